@@ -523,7 +523,9 @@ int plan_route(int T, int E, int K, bool dsv3, int &tok_per_wg) {
     if ((T + n - 1) / n > mx) return 0;
   }
   tok_per_wg = (T + n - 1) / n;
-  return n;
+  // the rounding up can cover the batch with fewer workgroups: one that starts past the
+  // last token must not run (its token count would be negative)
+  return (T + tok_per_wg - 1) / tok_per_wg;
 }
 
 template <int EPL>

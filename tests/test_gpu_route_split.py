@@ -1,0 +1,31 @@
+"""The routing call on batches whose tokens do not split evenly over its workgroups."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from gpu_util import dev, t16
+from mixture_experts_ffn_02_amd import moe_lora as ml
+from synth import Workload, make_config
+
+pytestmark = pytest.mark.gpu
+
+
+def test_batch_covered_by_fewer_workgroups_than_planned():
+    """16449 tokens: 256 workgroups are planned at 65 tokens each, 254 of which cover the batch;
+    none may start past its end."""
+    cfg = make_config(T=16449, H=8, I=8, E=32, top_k=2)
+    bits = Workload(cfg).logits()
+    T, E, k = cfg.T, cfg.E, cfg.top_k
+    d = ml.dims(T, 8, 8, E, k)
+    i32 = dict(dtype=torch.int32, device=dev())
+    ids, off, e2p, p2e = (torch.empty(s, **i32) for s in ((T, k), (E + 1,), (T * k,), (T * k,)))
+    w = torch.empty((T, k), device=dev())
+    ws = torch.empty((ml.moe_lora_route_workspace_size(d),), dtype=torch.uint8, device=dev())
+    ml.moe_lora_route(d, t16(bits), ids, w, off, e2p, p2e, ws)
+    want_ids, _ = oracle.route(bits, k)
+    want = oracle.expert_sort(want_ids, E)
+    assert np.array_equal(ids.cpu().numpy(), want_ids)
+    for got, exp in zip((off, e2p, p2e), want):
+        assert np.array_equal(got.cpu().numpy(), exp)
