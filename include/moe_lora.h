@@ -172,6 +172,55 @@ int moe_lora_route(const moe_lora_dims *dims, int routing, const moe_lora_groupe
                    int32_t *permuted_to_expanded, void *ws, size_t ws_bytes,
                    moe_lora_stream_t stream);
 
+/* ---------------------------------------------------------------- route, general scores
+ * moe_lora_route for routers of any of these forms, with the same outputs (so permute,
+ * forward and finalize follow it unchanged):
+ *   p = softmax over the E logits, or sigmoid of each;
+ *   key = p + bias where there is a bias, else the logit itself (p grows with it);
+ *   n_group > 1: groups are contiguous blocks of E / n_group experts scored by their
+ *     largest key (group_score 1) or the sum of their two largest (2: of p, without a bias);
+ *     the topk_group best are kept (ties -> lower group index);
+ *   the top_k keys among the kept groups are chosen (ties -> lower expert index);
+ *   weight = scale * p, or scale * p / (sum of the chosen p) with renormalize.
+ * Keys with a bias, and groups scored by two, are compared in fp64; weights are fp32.
+ * A logit of -inf masks its expert: it is chosen only where fewer than top_k others are
+ * left, with weight 0; a token whose experts are all masked has weights 0.  A NaN counts as
+ * the largest key, and its token's weights follow the formula; ids are always distinct and
+ * in range.
+ * Limits: num_tokens <= 65536 (MOE_LORA_ERR_UNSUPPORTED; route larger batches in chunks).
+ * dims: num_tokens, num_experts and top_k are used (hidden and inter only checked).
+ * Workspace: moe_lora_route_scored_workspace_size bytes (0 up to 64 tokens: one launch;
+ * larger batches take two). */
+typedef enum { MOE_LORA_SCORE_SOFTMAX = 0, MOE_LORA_SCORE_SIGMOID = 1 } moe_lora_score;
+typedef enum { MOE_LORA_DTYPE_BF16 = 0, MOE_LORA_DTYPE_F32 = 1 } moe_lora_dtype;
+
+typedef struct {
+  int32_t score;        /* moe_lora_score */
+  int32_t logits_dtype; /* moe_lora_dtype of the logits (and of their gradient) */
+  int32_t renormalize;  /* 0 or 1 */
+  int32_t n_group;      /* 1 = no groups; E % n_group == 0, n_group <= 64 */
+  int32_t topk_group;   /* 1 <= topk_group <= n_group */
+  int32_t group_score;  /* 1 or 2 experts make a group's score */
+  float scale;          /* factor of every weight */
+  const float *bias;    /* [E] fp32, selection only; NULL = none */
+} moe_lora_scoring;
+
+size_t moe_lora_route_scored_workspace_size(const moe_lora_dims *dims, const moe_lora_scoring *scoring);
+int moe_lora_route_scored(const moe_lora_dims *dims, const moe_lora_scoring *scoring,
+                          const void *logits, int32_t *topk_ids, float *topk_weights,
+                          int32_t *expert_offsets, int32_t *expanded_to_permuted,
+                          int32_t *permuted_to_expanded, void *ws, size_t ws_bytes,
+                          moe_lora_stream_t stream);
+
+/* Gradient of the weights to the logits: d_logits [T, E] (logits_dtype, every element
+ * written) from d_weights [T, k] fp32 for the given choice topk_ids [T, k].  The choice
+ * itself has no gradient and the bias takes none.  Softmax without renormalisation reaches
+ * every expert; the other forms only the chosen ones.  An id outside [0, E) takes no part;
+ * equal ids of one token add up.  Groups, bias and their checks do not apply here. */
+int moe_lora_route_scored_backward(const moe_lora_dims *dims, const moe_lora_scoring *scoring,
+                                   const void *logits, const int32_t *topk_ids,
+                                   const float *d_weights, void *d_logits, moe_lora_stream_t stream);
+
 /* ---------------------------------------------------------------- permute
  * x_perm[p, :] = x[permuted_to_expanded[p] / top_k, :]  (bf16 gather; the bf16 PR's
  * "permute bf16 hidden" step).  x [T, H], x_perm [T*k, H]. */

@@ -26,6 +26,11 @@ NOALLOC_SCRATCH_BYTES = 64 << 20
 ROUTING_RENORMALIZE = 0
 ROUTING_DEEPSEEK_V3 = 1
 
+SCORE_SOFTMAX = 0
+SCORE_SIGMOID = 1
+DTYPE_BF16 = 0
+DTYPE_F32 = 1
+
 LIB_NAME = "libmoe_lora.so"
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), LIB_NAME)
 
@@ -35,6 +40,9 @@ EXPORTED = (
     "moe_lora_version",
     "moe_lora_route_workspace_size",
     "moe_lora_route",
+    "moe_lora_route_scored_workspace_size",
+    "moe_lora_route_scored",
+    "moe_lora_route_scored_backward",
     "moe_lora_permute",
     "moe_lora_forward_workspace_size",
     "moe_lora_forward",
@@ -54,6 +62,12 @@ class Dims(ctypes.Structure):
 class Grouped(ctypes.Structure):
     _fields_ = [("n_group", c_int32), ("topk_group", c_int32),
                 ("routed_scaling_factor", c_float), ("correction_bias", c_void_p)]
+
+
+class ScoringC(ctypes.Structure):
+    _fields_ = [("score", c_int32), ("logits_dtype", c_int32), ("renormalize", c_int32),
+                ("n_group", c_int32), ("topk_group", c_int32), ("group_score", c_int32),
+                ("scale", c_float), ("bias", c_void_p)]
 
 
 class Adapters(ctypes.Structure):
@@ -103,6 +117,14 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_lora_route.argtypes = [POINTER(Dims), c_int, POINTER(Grouped), c_void_p, c_void_p,
                                    c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
                                    c_void_p]
+    lib.moe_lora_route_scored_workspace_size.restype = c_size_t
+    lib.moe_lora_route_scored_workspace_size.argtypes = [POINTER(Dims), POINTER(ScoringC)]
+    lib.moe_lora_route_scored.restype = c_int
+    lib.moe_lora_route_scored.argtypes = [POINTER(Dims), POINTER(ScoringC), c_void_p, c_void_p, c_void_p,
+                                          c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]
+    lib.moe_lora_route_scored_backward.restype = c_int
+    lib.moe_lora_route_scored_backward.argtypes = [POINTER(Dims), POINTER(ScoringC), c_void_p, c_void_p,
+                                                   c_void_p, c_void_p, c_void_p]
     lib.moe_lora_permute.restype = c_int
     lib.moe_lora_permute.argtypes = [POINTER(Dims), c_void_p, c_void_p, c_void_p, c_void_p]
     lib.moe_lora_forward_workspace_size.restype = c_size_t

@@ -148,6 +148,101 @@ int moe_lora_route(const moe_lora_dims *d, int routing, const moe_lora_grouped *
   return moe::launch_route(a, s);
 }
 
+namespace {
+
+// the parts of a scoring that both directions use
+int check_scoring(const moe_lora_dims *d, const moe_lora_scoring *sc) {
+  const int st = check_dims(d);
+  if (st != MOE_LORA_OK) return st;
+  if (!sc) return MOE_LORA_ERR_INVALID_ARGUMENT;
+  if (sc->score != MOE_LORA_SCORE_SOFTMAX && sc->score != MOE_LORA_SCORE_SIGMOID)
+    return MOE_LORA_ERR_INVALID_ARGUMENT;
+  if (sc->logits_dtype != MOE_LORA_DTYPE_BF16 && sc->logits_dtype != MOE_LORA_DTYPE_F32)
+    return MOE_LORA_ERR_INVALID_ARGUMENT;
+  if (sc->renormalize != 0 && sc->renormalize != 1) return MOE_LORA_ERR_INVALID_ARGUMENT;
+  if (d->num_tokens > moe::scored_max_tokens()) return MOE_LORA_ERR_UNSUPPORTED;
+  return MOE_LORA_OK;
+}
+
+int check_groups(const moe_lora_dims *d, const moe_lora_scoring *sc) {
+  const int E = d->num_experts;
+  if (sc->n_group <= 0 || sc->n_group > 64 || E % sc->n_group != 0) return MOE_LORA_ERR_INVALID_ARGUMENT;
+  if (sc->topk_group <= 0 || sc->topk_group > sc->n_group) return MOE_LORA_ERR_INVALID_ARGUMENT;
+  if (d->top_k > sc->topk_group * (E / sc->n_group)) return MOE_LORA_ERR_INVALID_ARGUMENT;
+  if (sc->group_score != 1 && sc->group_score != 2) return MOE_LORA_ERR_INVALID_ARGUMENT;
+  return MOE_LORA_OK;
+}
+
+}  // namespace
+
+size_t moe_lora_route_scored_workspace_size(const moe_lora_dims *d, const moe_lora_scoring *sc) {
+  if (check_scoring(d, sc) != MOE_LORA_OK || check_groups(d, sc) != MOE_LORA_OK || d->num_tokens == 0) return 0;
+  return moe::scored_workspace_bytes(d->num_tokens, d->num_experts, d->top_k, sc->n_group > 1);
+}
+
+int moe_lora_route_scored(const moe_lora_dims *d, const moe_lora_scoring *sc, const void *logits,
+                          int32_t *topk_ids, float *topk_weights, int32_t *expert_offsets, int32_t *e2p,
+                          int32_t *p2e, void *ws, size_t ws_bytes, moe_lora_stream_t stream) {
+  int st = check_scoring(d, sc);
+  if (st != MOE_LORA_OK || (st = check_groups(d, sc)) != MOE_LORA_OK) return st;
+  if (sc->bias && !aligned16(sc->bias)) return MOE_LORA_ERR_INVALID_ARGUMENT;
+  if (!expert_offsets || !aligned16(expert_offsets)) return MOE_LORA_ERR_INVALID_ARGUMENT;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const int E = d->num_experts;
+  if (d->num_tokens == 0) return moe::launch_zero_offsets(expert_offsets, E, s);
+  if (!logits || !topk_ids || !topk_weights || !e2p || !p2e || !aligned16(logits) || !aligned16(topk_ids) ||
+      !aligned16(topk_weights) || !aligned16(e2p) || !aligned16(p2e))
+    return MOE_LORA_ERR_INVALID_ARGUMENT;
+  const size_t need = moe::scored_workspace_bytes(d->num_tokens, E, d->top_k, sc->n_group > 1);
+  if (ws_bytes < need) return MOE_LORA_ERR_WORKSPACE_TOO_SMALL;
+  if (need > 0 && (!ws || !aligned16(ws))) return MOE_LORA_ERR_INVALID_ARGUMENT;
+  moe::RouteArgs a{};
+  a.logits = static_cast<const uint16_t *>(logits);
+  a.T = d->num_tokens;
+  a.E = E;
+  a.K = d->top_k;
+  a.n_group = sc->n_group;
+  a.topk_group = sc->topk_group;
+  a.ids = topk_ids;
+  a.weights = topk_weights;
+  a.offsets = expert_offsets;
+  a.e2p = e2p;
+  a.p2e = p2e;
+  a.hist = static_cast<int32_t *>(ws);
+  moe::ScoredArgs b{};
+  b.score = sc->score;
+  b.f32 = sc->logits_dtype == MOE_LORA_DTYPE_F32;
+  b.renormalize = sc->renormalize != 0;
+  b.group_score = sc->group_score;
+  b.scale = sc->scale;
+  b.bias = sc->bias;
+  return moe::launch_route_scored(a, b, s);
+}
+
+int moe_lora_route_scored_backward(const moe_lora_dims *d, const moe_lora_scoring *sc, const void *logits,
+                                   const int32_t *topk_ids, const float *d_weights, void *d_logits,
+                                   moe_lora_stream_t stream) {
+  const int st = check_scoring(d, sc);
+  if (st != MOE_LORA_OK) return st;
+  if (d->num_tokens == 0) return MOE_LORA_OK;
+  if (!logits || !topk_ids || !d_weights || !d_logits || !aligned16(logits) || !aligned16(topk_ids) ||
+      !aligned16(d_weights) || !aligned16(d_logits))
+    return MOE_LORA_ERR_INVALID_ARGUMENT;
+  moe::ScoredBackwardArgs a{};
+  a.logits = logits;
+  a.ids = topk_ids;
+  a.d_weights = d_weights;
+  a.d_logits = d_logits;
+  a.T = d->num_tokens;
+  a.E = d->num_experts;
+  a.K = d->top_k;
+  a.score = sc->score;
+  a.f32 = sc->logits_dtype == MOE_LORA_DTYPE_F32;
+  a.renormalize = sc->renormalize != 0;
+  a.scale = sc->scale;
+  return moe::launch_route_scored_backward(a, reinterpret_cast<hipStream_t>(stream));
+}
+
 int moe_lora_permute(const moe_lora_dims *d, const uint16_t *x, const int32_t *p2e,
                      uint16_t *x_perm, moe_lora_stream_t stream) {
   int st = check_dims(d);

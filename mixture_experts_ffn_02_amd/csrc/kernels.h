@@ -11,7 +11,7 @@ namespace moe {
 
 // ---- routing ------------------------------------------------------------
 struct RouteArgs {
-  const uint16_t *logits;
+  const uint16_t *logits;  // (general routing: bf16 or fp32)
   int T, E, K;
   int method;  // moe_lora_routing
   int n_group, topk_group;
@@ -28,6 +28,31 @@ size_t route_workspace_bytes(int T, int E, int K);
 int route_max_tokens(int E, int K, bool dsv3);
 int launch_route(const RouteArgs &a, hipStream_t s);
 int launch_zero_offsets(int32_t *offsets, int E, hipStream_t s);
+
+// ---- general routing (scores, bias, groups) ---------------------------------
+struct ScoredArgs {
+  int score;  // moe_lora_score
+  bool f32;   // fp32 logits (else bf16)
+  bool renormalize;
+  int group_score;
+  float scale;
+  const float *bias;
+};
+struct ScoredBackwardArgs {
+  const void *logits;
+  const int32_t *ids;
+  const float *d_weights;
+  void *d_logits;
+  int T, E, K;
+  int score;
+  bool f32, renormalize;
+  float scale;
+};
+size_t scored_workspace_bytes(int T, int E, int K, bool groups);
+int scored_max_tokens();
+// RouteArgs: logits (either type), sizes, groups and outputs; method, rsf and bias unused
+int launch_route_scored(const RouteArgs &a, const ScoredArgs &s, hipStream_t st);
+int launch_route_scored_backward(const ScoredBackwardArgs &a, hipStream_t s);
 
 // ---- permute / finalize ---------------------------------------------------
 int launch_permute(const uint16_t *x, const int32_t *p2e, uint16_t *x_perm, int R, int H, int K,

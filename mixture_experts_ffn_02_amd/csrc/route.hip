@@ -24,21 +24,14 @@
 //   the expert id, the base from the per-wave, per-workgroup prefix counts.
 #include "common.h"
 #include "kernels.h"
+#include "route_pack.h"
 
 namespace moe {
 namespace {
 
-constexpr int kRouteThreads = 1024;
 constexpr int kRouteWaves = kRouteThreads / 64;
 constexpr int kSingleMaxT = 64;     // one workgroup handles the whole batch up to this
 constexpr int kMaxTokPerWg = 256;   // LDS bound of the per-workgroup id buffer
-constexpr int kMaxRouteWg = 256;    // workgroups of one routing launch
-
-struct RouteParams {
-  RouteArgs a;
-  int tok_per_wg;
-  int num_wg;
-};
 
 MOE_DEV uint32_t bf16_order_key(uint32_t b) {
   b &= 0xffffu;
@@ -331,80 +324,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteParams P) {
   }
   __syncthreads();
 
-  // ---- per-wave starting positions inside this workgroup, workgroup totals
-  for (int e = tid; e < E; e += kRouteThreads) {
-    int run = 0;
-    for (int w = 0; w < kRouteWaves; ++w) {
-      const int c = hist_w[w * E + e];
-      hist_w[w * E + e] = run;
-      run += c;
-    }
-    tot[e] = run;
-    if (MULTI) a.hist[(size_t)blockIdx.x * E + e] = run;
-  }
-  __syncthreads();
-  if (!MULTI && wave == 0) {
-    // one workgroup: offsets are the exclusive scan of its totals
-    const int per_lane = (E + 63) / 64;
-    int local = 0;
-    for (int q = 0; q < per_lane; ++q) {
-      const int e = lane * per_lane + q;
-      local += (e < E) ? tot[e] : 0;
-    }
-    int incl = local;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int o = __shfl_up(incl, off);
-      if (lane >= off) incl += o;
-    }
-    int run = incl - local;
-    for (int q = 0; q < per_lane; ++q) {
-      const int e = lane * per_lane + q;
-      if (e < E) {
-        a.offsets[e] = run;
-        wgbase[e] = run;
-        run += tot[e];
-      }
-    }
-    if (lane == 63) a.offsets[E] = incl;
-  }
-  if (MULTI)
-    for (int e = tid; e < E; e += kRouteThreads) wgbase[e] = 0;
-  __syncthreads();
-
-  // ---- stable scatter of this wave's expanded rows.  One workgroup writes final
-  // positions; with several, each writes its positions relative to its own block
-  // (into e2p) and the last workgroup to finish adds the global bases.
-  int32_t *start = hist_w + wave * E;
-  const int j0 = w_begin * K, j1 = w_end * K;
-  const int jl0 = t_begin * K;
-  int nbits = 0;
-  while ((1 << nbits) < E) ++nbits;
-  const uint64_t lt = (lane == 0) ? 0ull : (~0ull >> (64 - lane));
-  for (int base = j0; base < j1; base += 64) {
-    const int j = base + lane;
-    const bool valid = j < j1;
-    const int e = valid ? ids_l[j - jl0] : 0;
-    uint64_t peers = __ballot(valid);
-    for (int bb = 0; bb < nbits; ++bb) {
-      const bool bit = (e >> bb) & 1;
-      const uint64_t m = __ballot(valid && bit);
-      peers &= bit ? m : ~m;
-    }
-    const int rank = __popcll(peers & lt);
-    int sp = 0;
-    if (valid) sp = start[e];
-    __builtin_amdgcn_wave_barrier();
-    if (valid) {
-      const int pos = wgbase[e] + sp + rank;
-      a.e2p[j] = pos;
-      if (!MULTI) a.p2e[pos] = j;
-      if ((peers & lt) == 0ull) start[e] = sp + __popcll(peers);
-    }
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-  }
+  pack_block<MULTI>(a, hist_w, ids_l, tot, wgbase, kRouteWaves, kRouteThreads, t_begin, w_begin, w_end);
 }
 
 // Second launch for multi-workgroup batches: every workgroup reads all per-workgroup
@@ -545,11 +465,15 @@ int launch_epl(const RouteArgs &a, hipStream_t s) {
   if (!allow_lds<EPL, true>(lds)) return ST_HIP;
   route_kernel<EPL, true><<<nwg, kRouteThreads, lds, s>>>(P);
   if (hipGetLastError() != hipSuccess) return ST_HIP;
-  route_finish_kernel<<<nwg, kRouteThreads, 0, s>>>(P);
-  return hipGetLastError() == hipSuccess ? ST_OK : ST_HIP;
+  return launch_route_finish(P, s);
 }
 
 }  // namespace
+
+int launch_route_finish(const RouteParams &P, hipStream_t s) {
+  route_finish_kernel<<<P.num_wg, kRouteThreads, 0, s>>>(P);
+  return hipGetLastError() == hipSuccess ? ST_OK : ST_HIP;
+}
 
 size_t route_workspace_bytes(int T, int E, int K) {
   // enough for either routing method

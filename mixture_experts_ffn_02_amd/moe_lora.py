@@ -153,6 +153,102 @@ def moe_lora_finalize(d: Dims, y_perm, topk_weights, e2p, out, stream=None) -> N
         ctypes.byref(d), _ptr(y_perm), _ptr(topk_weights), _ptr(e2p), _ptr(out), _stream(stream)))
 
 
+# ---- operators around the expert layer.  These check every tensor (device, type, shape,
+# contiguity) before the call, and launch on the tensors' device.
+
+def _on(*tensors):
+    """The one device of these tensors; they must all be on it."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if dev is None:
+            dev = t.device
+            if dev.type != "cuda":
+                raise ValueError(f"a GPU tensor is needed, got one on {dev}")
+        elif t.device != dev:
+            raise ValueError(f"tensors of one call are on {dev} and {t.device}")
+    return dev
+
+
+def _checked(name: str, t: torch.Tensor, dtype, numel: int) -> int:
+    """Data pointer of a contiguous tensor of this type and size."""
+    if t.dtype is not dtype and not (dtype is torch.bfloat16 and t.dtype in (torch.int16, torch.uint16)):
+        raise ValueError(f"{name}: {dtype} expected, got {t.dtype}")
+    if t.numel() != numel:
+        raise ValueError(f"{name}: {numel} elements expected, got shape {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor is needed")
+    return t.data_ptr()
+
+
+def _call(fn: str, dev, stream, *args) -> None:
+    """The library call with the tensors' device current (its kernels launch there), on the
+    given stream or that device's current one."""
+    if dev is not None and dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            check(fn, getattr(load(), fn)(*args, _stream(stream)))
+    else:
+        check(fn, getattr(load(), fn)(*args, _stream(stream)))
+
+
+@dataclass
+class Scoring:
+    """How moe_lora_route_scored scores, groups and weights the experts.
+
+    score: "softmax" or "sigmoid"; bias: [E] fp32, added to the scores for the choice only;
+    group_score: how many of a group's best experts make its score (1 or 2).
+    """
+
+    score: str = "softmax"
+    renormalize: bool = True
+    n_group: int = 1
+    topk_group: int = 1
+    group_score: int = 1
+    scale: float = 1.0
+    bias: Optional[torch.Tensor] = None
+
+    def to_c(self, logits_dtype: torch.dtype, num_experts: int) -> _lib.ScoringC:
+        if self.score not in ("softmax", "sigmoid"):
+            raise ValueError(f"score: 'softmax' or 'sigmoid', got {self.score!r}")
+        f32 = logits_dtype is torch.float32
+        if not f32 and logits_dtype not in (torch.bfloat16, torch.int16, torch.uint16):
+            raise ValueError(f"logits are bf16 or fp32, got {logits_dtype}")
+        return _lib.ScoringC(
+            _lib.SCORE_SIGMOID if self.score == "sigmoid" else _lib.SCORE_SOFTMAX,
+            _lib.DTYPE_F32 if f32 else _lib.DTYPE_BF16, int(bool(self.renormalize)), self.n_group,
+            self.topk_group, self.group_score, self.scale,
+            None if self.bias is None else _checked("bias", self.bias, torch.float32, num_experts))
+
+
+def moe_lora_route_scored_workspace_size(d: Dims, scoring: Scoring, logits_dtype=torch.bfloat16) -> int:
+    return int(load().moe_lora_route_scored_workspace_size(
+        ctypes.byref(d), ctypes.byref(scoring.to_c(logits_dtype, d.num_experts))))
+
+
+def moe_lora_route_scored(d: Dims, scoring: Scoring, logits, topk_ids, topk_weights, expert_offsets, e2p, p2e,
+                          ws, stream=None) -> None:
+    T, E, R = d.num_tokens, d.num_experts, d.num_tokens * d.top_k
+    sc = scoring.to_c(logits.dtype, E)
+    i32 = torch.int32
+    _call("moe_lora_route_scored",
+          _on(logits, topk_ids, topk_weights, expert_offsets, e2p, p2e, ws, scoring.bias), stream,
+          ctypes.byref(d), ctypes.byref(sc), _checked("logits", logits, logits.dtype, T * E),
+          _checked("topk_ids", topk_ids, i32, R), _checked("topk_weights", topk_weights, torch.float32, R),
+          _checked("expert_offsets", expert_offsets, i32, E + 1), _checked("e2p", e2p, i32, R),
+          _checked("p2e", p2e, i32, R), _ptr(ws), ws.numel() * ws.element_size() if ws is not None else 0)
+
+
+def moe_lora_route_scored_backward(d: Dims, scoring: Scoring, logits, topk_ids, d_weights, d_logits,
+                                   stream=None) -> None:
+    T, E, R = d.num_tokens, d.num_experts, d.num_tokens * d.top_k
+    sc = scoring.to_c(logits.dtype, E)
+    _call("moe_lora_route_scored_backward", _on(logits, topk_ids, d_weights, d_logits), stream,
+          ctypes.byref(d), ctypes.byref(sc), _checked("logits", logits, logits.dtype, T * E),
+          _checked("topk_ids", topk_ids, torch.int32, R), _checked("d_weights", d_weights, torch.float32, R),
+          _checked("d_logits", d_logits, logits.dtype, T * E))
+
+
 @dataclass
 class RouteOut:
     topk_ids: torch.Tensor
@@ -173,7 +269,8 @@ class MoELoRALayer:
     already packed.  With w_gate_up_scale / w_down_scale the expert weights are FP8: uint8
     E4M3 codes [E, 2I, H] / [E, H, I] with fp32 scales per 128 x 128 block, run through
     moe_lora_forward_fp8 (packed_weights / weights_prepacked then refer to the FP8
-    tile-packed layout of moe_lora_pack_weights_fp8).
+    tile-packed layout of moe_lora_pack_weights_fp8).  routing: one of the ROUTING_ methods,
+    or a Scoring (moe_lora_route_scored; logits bf16 or fp32).
     """
 
     def __init__(self, hidden: int, inter: int, num_experts: int, top_k: int,
@@ -219,6 +316,11 @@ class MoELoRALayer:
     def dims(self, T: int) -> Dims:
         return Dims(T, self.H, self.I, self.E, self.k)
 
+    def _route_workspace(self, d: Dims) -> int:
+        if isinstance(self.routing, Scoring):
+            return moe_lora_route_scored_workspace_size(d, self.routing)
+        return moe_lora_route_workspace_size(d)
+
     def _buffers(self, T: int, lora: Optional[Adapters], device) -> dict:
         key = (T, None if lora is None else tuple(lora.rank[: lora.num_slots]))
         b = self._bufs.get(key)
@@ -233,8 +335,7 @@ class MoELoRALayer:
                 "e2p": torch.empty((R,), **i32),
                 "p2e": torch.empty((R,), **i32),
                 # per-workgroup expert histograms of the two-launch routing (written before read)
-                "rws": torch.empty((max(1, moe_lora_route_workspace_size(d)),), dtype=torch.uint8,
-                                   device=device),
+                "rws": torch.empty((max(1, self._route_workspace(d)),), dtype=torch.uint8, device=device),
                 "fws": torch.empty((max(1, moe_lora_forward_workspace_size(d, lora)),),
                                    dtype=torch.uint8, device=device),
                 "x_perm": None if self.gather_on_load else torch.empty((R, self.H), dtype=torch.bfloat16,
@@ -251,8 +352,12 @@ class MoELoRALayer:
         c_lora = lora.to_c() if lora is not None else None
         b = self._buffers(T, c_lora, x.device)
         d = self.dims(T)
-        moe_lora_route(d, logits, b["ids"], b["w"], b["off"], b["e2p"], b["p2e"], b["rws"],
-                       self.routing, self.grouped, stream)
+        if isinstance(self.routing, Scoring):
+            moe_lora_route_scored(d, self.routing, logits, b["ids"], b["w"], b["off"], b["e2p"], b["p2e"],
+                                  b["rws"], stream)
+        else:
+            moe_lora_route(d, logits, b["ids"], b["w"], b["off"], b["e2p"], b["p2e"], b["rws"],
+                           self.routing, self.grouped, stream)
         if not self.gather_on_load:
             moe_lora_permute(d, x, b["p2e"], b["x_perm"], stream)
         if self.packed_weights or self.fp8_pow2_scales:

@@ -1,0 +1,117 @@
+"""The operators around the expert layer on the CPU: argument checks of the C calls (nothing is
+launched), checks of the binding, and the oracle's definitions against differences and
+against the layer's own oracle."""
+
+import ctypes
+import itertools
+
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_ffn_02_amd as pkg
+import oracle
+from mixture_experts_ffn_02_amd import _lib
+from mixture_experts_ffn_02_amd import moe_lora as ml
+from oracle import operators_ref as ref
+
+FAKE = 1 << 20  # 16-byte aligned, never dereferenced: validation fails first
+
+
+def _scoring(**kw):
+    v = dict(score=0, logits_dtype=0, renormalize=1, n_group=1, topk_group=1, group_score=1, scale=1.0, bias=None)
+    v.update(kw)
+    return _lib.ScoringC(*[v[f] for f, _ in _lib.ScoringC._fields_])
+
+
+def _route(d, sc, logits=FAKE, ws_bytes=1 << 30, ws=FAKE):
+    return pkg.load().moe_lora_route_scored(ctypes.byref(d), ctypes.byref(sc) if sc else None, logits, FAKE, FAKE, FAKE,
+                                            FAKE, FAKE, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("change", [dict(score=2), dict(score=-1), dict(logits_dtype=2), dict(renormalize=2),
+                                    dict(n_group=0), dict(n_group=3), dict(n_group=65), dict(n_group=4, topk_group=5),
+                                    dict(n_group=4, topk_group=0), dict(group_score=0), dict(group_score=3),
+                                    dict(n_group=4, topk_group=1), dict(bias=FAKE + 4)])
+def test_route_scored_refusals(change):
+    d = _lib.Dims(16, 8, 8, 8, 3)  # k = 3 does not fit one group of two experts
+    assert _route(d, _scoring(**change)) == _lib.ERR_INVALID_ARGUMENT
+
+
+def test_route_scored_refuses_bad_sizes_pointers_and_workspaces():
+    lib = pkg.load()
+    d = _lib.Dims(16, 8, 8, 8, 2)
+    assert _route(d, None) == _lib.ERR_INVALID_ARGUMENT
+    assert _route(d, _scoring(), logits=None) == _lib.ERR_INVALID_ARGUMENT
+    assert _route(d, _scoring(), logits=FAKE + 8) == _lib.ERR_INVALID_ARGUMENT
+    assert _route(_lib.Dims(65537, 8, 8, 8, 2), _scoring()) == _lib.ERR_UNSUPPORTED
+    assert _route(_lib.Dims(16, 8, 8, 513, 2), _scoring()) == _lib.ERR_INVALID_ARGUMENT
+    big = _lib.Dims(4096, 8, 8, 8, 2)
+    need = lib.moe_lora_route_scored_workspace_size(ctypes.byref(big), ctypes.byref(_scoring()))
+    assert need > 0
+    assert _route(big, _scoring(), ws_bytes=need - 1) == _lib.ERR_WORKSPACE_TOO_SMALL
+    assert _route(big, _scoring(), ws=None) == _lib.ERR_INVALID_ARGUMENT
+    assert lib.moe_lora_route_scored_workspace_size(ctypes.byref(d), ctypes.byref(_scoring())) == 0
+    for i in range(4):
+        args = [FAKE, FAKE, FAKE, FAKE]
+        args[i] = None
+        assert lib.moe_lora_route_scored_backward(ctypes.byref(d), ctypes.byref(_scoring()), *args, None) == \
+            _lib.ERR_INVALID_ARGUMENT
+    assert lib.moe_lora_route_scored_backward(ctypes.byref(_lib.Dims(0, 8, 8, 8, 2)), ctypes.byref(_scoring()), None,
+                                              None, None, None, None) == _lib.OK
+
+
+def test_scoring_descriptor_refusals():
+    with pytest.raises(ValueError, match="score"):
+        ml.Scoring(score="tanh").to_c(torch.bfloat16, 8)
+    with pytest.raises(ValueError, match="logits"):
+        ml.Scoring().to_c(torch.float16, 8)
+    with pytest.raises(ValueError, match="bias"):
+        ml.Scoring(bias=torch.zeros(7)).to_c(torch.bfloat16, 8)
+
+
+def test_binding_refuses_cpu_tensors_and_wrong_shapes():
+    t = torch.zeros((4, 8))
+    with pytest.raises(ValueError, match="GPU"):
+        ml.moe_lora_route_scored_backward(ml.dims(4, 8, 8, 8, 2), ml.Scoring(), t, t, t, t)
+    with pytest.raises(ValueError, match="elements"):
+        ml._checked("x", t, torch.float32, 33)
+    with pytest.raises(ValueError, match="float32"):
+        ml._checked("x", t.double(), torch.float32, 32)
+    with pytest.raises(ValueError, match="contiguous"):
+        ml._checked("x", t.t(), torch.float32, 32)
+
+
+# ---- the oracle's definitions
+def _logits(T, E, seed=0):
+    return np.random.Generator(np.random.PCG64(seed)).standard_normal((T, E)) * 1.5
+
+
+def test_scored_oracle_holds_the_named_methods():
+    bits = (np.float32(_logits(9, 32)).view(np.uint32) >> 16).astype(np.uint16)
+    l = oracle.bf16_bits_to_f64(bits)
+    ids, w = oracle.route(bits, 4)
+    got_ids, got_w = ref.route_scored(l, 4)
+    assert np.array_equal(ids, got_ids)
+    np.testing.assert_allclose(got_w, w, rtol=1e-12)
+    bias = np.float32(_logits(1, 32, 1)[0] * 0.1)
+    ids, w = oracle.route(bits, 4, "deepseek_v3", bias, 4, 2, 2.5)
+    got_ids, got_w = ref.route_scored(l, 4, "sigmoid", True, 4, 2, 2, 2.5, bias)
+    assert np.array_equal(ids, got_ids)
+    np.testing.assert_allclose(got_w, w, rtol=1e-12)
+
+
+@pytest.mark.parametrize("score,renorm", list(itertools.product(["softmax", "sigmoid"], [True, False])))
+def test_scored_gradient_equals_differences(score, renorm):
+    l = _logits(3, 7, 2)
+    ids = np.array([[1, 4, 6], [0, 2, 3], [5, 1, 0]])
+    dw = _logits(3, 3, 3)
+    got = ref.route_scored_backward(l, ids, dw, score, renorm, 1.5)
+    h = 1e-6
+    for t, e in itertools.product(range(3), range(7)):
+        up, down = l.copy(), l.copy()
+        up[t, e] += h
+        down[t, e] -= h
+        diff = 1.5 * (dw * (ref.chosen_weights(up, ids, score, renorm) -
+                            ref.chosen_weights(down, ids, score, renorm))).sum() / (2 * h)
+        assert abs(diff - got[t, e]) < 1e-7
