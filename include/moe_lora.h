@@ -354,6 +354,36 @@ int moe_lora_finalize(const moe_lora_dims *dims, const uint16_t *y_perm,
                       const float *topk_weights, const int32_t *expanded_to_permuted,
                       uint16_t *out, moe_lora_stream_t stream);
 
+/* ---------------------------------------------------------------- 8-bit checkpoints
+ * Rows of bf16 values kept in 8 bits for a backward pass: of each 32 neighbours of a row
+ * (the last block of a row may be shorter), e is the smallest exponent >= -117 with
+ * max|x| <= 448 * 2^e over the block's finite values, and the code is E4M3(x * 2^-e),
+ * rounded to nearest even.  The value is code * 2^e: off by at most 2^-4 of itself (or
+ * 2^-10 * 2^e below 2^(e-6)), and exact in bf16.
+ *   codes [rows, cols] OCP E4M3; exps [rows, ceil(cols / 32)]: e + 127, one byte each.
+ *   A NaN or an infinity becomes the code 0x7f (NaN); magnitudes above 240 * 2^120 are held
+ *   as that value (the next code's value is past bf16).  An exponent byte of 0 or 255 is
+ *   never written; reading one is not defined.
+ * cols: a multiple of 8 (else MOE_LORA_ERR_UNSUPPORTED), at most 65536; rows >= 0 and at most
+ * 2^31 - 1.  Device pointers 16-byte aligned; source and destination must not overlap. */
+int moe_lora_checkpoint_pack(int64_t rows, int32_t cols, const uint16_t *x, uint8_t *codes, uint8_t *exps,
+                             moe_lora_stream_t stream);
+int moe_lora_checkpoint_unpack(int64_t rows, int32_t cols, const uint8_t *codes, const uint8_t *exps,
+                               uint16_t *x, moe_lora_stream_t stream);
+
+/* ---------------------------------------------------------------- finalize, backward
+ * Gradients of moe_lora_finalize for d_out [T, H] bf16:
+ *   d_y_perm[e2p[t*k+j], :] = bf16(topk_weights[t, j] * d_out[t, :])          [T*k, H]
+ *   d_weights[t, j] = sum_h d_out[t, h] * y_perm[e2p[t*k+j], h]               [T, k] fp32
+ * (d_weights is what moe_lora_route_scored_backward takes.)  y_perm is given either in bf16
+ * or as its checkpoint (y_codes and y_exps of T*k rows, y_perm NULL); giving both or neither
+ * is MOE_LORA_ERR_INVALID_ARGUMENT.  A position outside [0, T*k) takes no part (its weight's
+ * gradient is 0); rows that no position names are left as they were. */
+int moe_lora_finalize_backward(const moe_lora_dims *dims, const uint16_t *d_out, const uint16_t *y_perm,
+                               const uint8_t *y_codes, const uint8_t *y_exps, const float *topk_weights,
+                               const int32_t *expanded_to_permuted, uint16_t *d_y_perm,
+                               float *d_weights, moe_lora_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_float, c_int, c_int32, c_size_t, c_void_p
+from ctypes import POINTER, c_float, c_int, c_int32, c_int64, c_size_t, c_void_p
 
 MAX_SLOTS = 8
 MAX_RANK = 64
@@ -51,6 +51,9 @@ EXPORTED = (
     "moe_lora_pack_weights",
     "moe_lora_pack_weights_fp8",
     "moe_lora_finalize",
+    "moe_lora_finalize_backward",
+    "moe_lora_checkpoint_pack",
+    "moe_lora_checkpoint_unpack",
 )
 
 
@@ -151,6 +154,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_lora_finalize.restype = c_int
     lib.moe_lora_finalize.argtypes = [POINTER(Dims), c_void_p, c_void_p, c_void_p, c_void_p,
                                       c_void_p]
+    lib.moe_lora_finalize_backward.restype = c_int
+    lib.moe_lora_finalize_backward.argtypes = [POINTER(Dims)] + [c_void_p] * 9
+    for name in ("moe_lora_checkpoint_pack", "moe_lora_checkpoint_unpack"):
+        getattr(lib, name).restype = c_int
+        getattr(lib, name).argtypes = [c_int64, c_int32, c_void_p, c_void_p, c_void_p, c_void_p]
     _lib = lib
     return lib
 

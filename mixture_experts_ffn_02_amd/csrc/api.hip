@@ -389,4 +389,53 @@ int moe_lora_finalize(const moe_lora_dims *d, const uint16_t *y_perm, const floa
                               reinterpret_cast<hipStream_t>(stream));
 }
 
+namespace {
+
+int check_checkpoint(int64_t rows, int32_t cols) {
+  if (rows < 0 || cols <= 0) return MOE_LORA_ERR_INVALID_ARGUMENT;
+  if (cols % 8 != 0 || cols > 65536 || rows > 0x7fffffffll) return MOE_LORA_ERR_UNSUPPORTED;
+  return MOE_LORA_OK;
+}
+
+}  // namespace
+
+int moe_lora_checkpoint_pack(int64_t rows, int32_t cols, const uint16_t *x, uint8_t *codes, uint8_t *exps,
+                             moe_lora_stream_t stream) {
+  const int st = check_checkpoint(rows, cols);
+  if (st != MOE_LORA_OK) return st;
+  if (rows == 0) return MOE_LORA_OK;
+  if (!x || !codes || !exps || !aligned16(x) || !aligned16(codes) || !aligned16(exps))
+    return MOE_LORA_ERR_INVALID_ARGUMENT;
+  return moe::launch_checkpoint_pack(rows, cols, x, codes, exps, reinterpret_cast<hipStream_t>(stream));
+}
+
+int moe_lora_checkpoint_unpack(int64_t rows, int32_t cols, const uint8_t *codes, const uint8_t *exps, uint16_t *x,
+                               moe_lora_stream_t stream) {
+  const int st = check_checkpoint(rows, cols);
+  if (st != MOE_LORA_OK) return st;
+  if (rows == 0) return MOE_LORA_OK;
+  if (!x || !codes || !exps || !aligned16(x) || !aligned16(codes) || !aligned16(exps))
+    return MOE_LORA_ERR_INVALID_ARGUMENT;
+  return moe::launch_checkpoint_unpack(rows, cols, codes, exps, x, reinterpret_cast<hipStream_t>(stream));
+}
+
+int moe_lora_finalize_backward(const moe_lora_dims *d, const uint16_t *d_out, const uint16_t *y_perm,
+                               const uint8_t *y_codes, const uint8_t *y_exps, const float *topk_weights,
+                               const int32_t *e2p, uint16_t *d_y_perm, float *d_weights,
+                               moe_lora_stream_t stream) {
+  const int st = check_dims(d);
+  if (st != MOE_LORA_OK) return st;
+  if (d->num_tokens == 0) return MOE_LORA_OK;
+  const bool codes = y_codes || y_exps;
+  if (codes == (y_perm != nullptr) || (codes && (!y_codes || !y_exps))) return MOE_LORA_ERR_INVALID_ARGUMENT;
+  if (!d_out || !topk_weights || !e2p || !d_y_perm || !d_weights) return MOE_LORA_ERR_INVALID_ARGUMENT;
+  if (!aligned16(d_out) || !aligned16(y_perm) || !aligned16(y_codes) || !aligned16(y_exps) ||
+      !aligned16(topk_weights) || !aligned16(e2p) || !aligned16(d_y_perm) || !aligned16(d_weights))
+    return MOE_LORA_ERR_INVALID_ARGUMENT;
+  moe::FinalizeBackwardArgs a{d_out,    y_perm,    y_codes, y_exps,    topk_weights,
+                              e2p,      d_y_perm,  d_weights, d->num_tokens, d->hidden,
+                              d->top_k, d->num_tokens * d->top_k};
+  return moe::launch_finalize_backward(a, reinterpret_cast<hipStream_t>(stream));
+}
+
 }  // extern "C"

@@ -60,6 +60,24 @@ int launch_permute(const uint16_t *x, const int32_t *p2e, uint16_t *x_perm, int 
 int launch_finalize(const uint16_t *y_perm, const float *w, const int32_t *e2p, uint16_t *out,
                     int T, int H, int K, hipStream_t s);
 
+struct FinalizeBackwardArgs {
+  const uint16_t *d_out;  // [T, H]
+  const uint16_t *y;      // [R, H], or NULL with the checkpoint
+  const uint8_t *codes;   // [R, H]
+  const uint8_t *exps;    // [R, ceil(H / 32)]
+  const float *w;         // [T, K]
+  const int32_t *e2p;     // [T * K]
+  uint16_t *d_y;          // [R, H]
+  float *d_w;             // [T, K]
+  int T, H, K, R;
+};
+int launch_finalize_backward(const FinalizeBackwardArgs &a, hipStream_t s);
+
+// ---- 8-bit checkpoints ------------------------------------------------------------
+int launch_checkpoint_pack(long long rows, int cols, const uint16_t *x, uint8_t *codes, uint8_t *exps, hipStream_t s);
+int launch_checkpoint_unpack(long long rows, int cols, const uint8_t *codes, const uint8_t *exps, uint16_t *x,
+                             hipStream_t s);
+
 // ---- tile-packed expert weights ---------------------------------------------------
 int launch_pack_weights_fp8(const moe_lora_dims &d, const uint8_t *w1, const uint8_t *w2, uint8_t *w1p,
                             uint8_t *w2p, hipStream_t s);

@@ -7,6 +7,7 @@
 //
 // Both kernels are HBM-bound row copies: one wavefront moves one 16-byte vector per
 // lane per step, so every row is read and written with fully coalesced accesses.
+#include "checkpoint.h"
 #include "common.h"
 #include "kernels.h"
 
@@ -63,7 +64,90 @@ __global__ __launch_bounds__(kRowThreads) void finalize_kernel(const uint16_t *_
   }
 }
 
+// Gradients of finalize: d_y[e2p[t k + j], :] = w[t, j] d_out[t, :] and
+// d_w[t, j] = <d_out[t], y[e2p[t k + j]]>.  One workgroup per token; its four wavefronts
+// split the k choices, and a wavefront walks the row in 512-wide pieces with the piece of
+// d_out in registers for all of its choices (JN of them).  Products and sums in fp32, a
+// row's sum in a fixed order.  Bound by HBM: the routed rows are read once (2 bytes a
+// value, 1 + 1/32 from a checkpoint) and written once.
+template <int JN, bool CODES>
+__global__ __launch_bounds__(kRowThreads) void finalize_backward_kernel(const FinalizeBackwardArgs P) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int t = blockIdx.x, H = P.H, K = P.K;
+  const int nb = (H + kCkptBlock - 1) / kCkptBlock;
+  long long row[JN];
+  float w[JN], dot[JN];
+  bool on[JN];
+#pragma unroll
+  for (int i = 0; i < JN; ++i) {
+    const int j = wave * JN + i;
+    const int p = j < K ? P.e2p[(size_t)t * K + j] : -1;
+    on[i] = p >= 0 && p < P.R;  // (a position outside the routed rows takes no part)
+    row[i] = on[i] ? p : 0;
+    w[i] = on[i] ? P.w[(size_t)t * K + j] : 0.f;
+    dot[i] = 0.f;
+  }
+  for (int h = lane * 8; h < H; h += 512) {
+    const u32x4_t d4 = *reinterpret_cast<const u32x4_t *>(P.d_out + (size_t)t * H + h);
+    u32x4_t y4[JN];
+#pragma unroll
+    for (int i = 0; i < JN; ++i) {
+      if (!on[i]) continue;
+      if constexpr (CODES) {
+        const u32x2_t c = *reinterpret_cast<const u32x2_t *>(P.codes + row[i] * H + h);
+        y4[i] = ckpt_to_bf16(c, ckpt_scale(P.exps[row[i] * nb + h / kCkptBlock]));
+      } else {
+        y4[i] = *reinterpret_cast<const u32x4_t *>(P.y + row[i] * H + h);
+      }
+    }
+    float d[8];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      d[2 * c] = bf16_to_f32(d4[c] & 0xffffu);
+      d[2 * c + 1] = bf16_to_f32(d4[c] >> 16);
+    }
+#pragma unroll
+    for (int i = 0; i < JN; ++i) {
+      if (!on[i]) continue;
+      u32x4_t o;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        dot[i] += d[2 * c] * bf16_to_f32(y4[i][c] & 0xffffu);
+        dot[i] += d[2 * c + 1] * bf16_to_f32(y4[i][c] >> 16);
+        o[c] = pack_bf16x2(w[i] * d[2 * c], w[i] * d[2 * c + 1]);
+      }
+      *reinterpret_cast<u32x4_t *>(P.d_y + row[i] * H + h) = o;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < JN; ++i) {
+    float v = dot[i];
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
+    const int j = wave * JN + i;
+    if (lane == 0 && j < K) P.d_w[(size_t)t * K + j] = v;
+  }
+}
+
+template <bool CODES>
+int launch_fin_bwd(const FinalizeBackwardArgs &a, hipStream_t s) {
+  const int per = (a.K + 3) / 4;
+  if (per <= 1)
+    finalize_backward_kernel<1, CODES><<<a.T, kRowThreads, 0, s>>>(a);
+  else if (per <= 2)
+    finalize_backward_kernel<2, CODES><<<a.T, kRowThreads, 0, s>>>(a);
+  else if (per <= 4)
+    finalize_backward_kernel<4, CODES><<<a.T, kRowThreads, 0, s>>>(a);
+  else
+    finalize_backward_kernel<8, CODES><<<a.T, kRowThreads, 0, s>>>(a);
+  return hipGetLastError() == hipSuccess ? ST_OK : ST_HIP;
+}
+
 }  // namespace
+
+int launch_finalize_backward(const FinalizeBackwardArgs &a, hipStream_t s) {
+  return a.codes ? launch_fin_bwd<true>(a, s) : launch_fin_bwd<false>(a, s);
+}
 
 int launch_permute(const uint16_t *x, const int32_t *p2e, uint16_t *x_perm, int R, int H, int K,
                    hipStream_t s) {

@@ -249,6 +249,47 @@ def moe_lora_route_scored_backward(d: Dims, scoring: Scoring, logits, topk_ids, 
           _checked("d_logits", d_logits, logits.dtype, T * E))
 
 
+def _rows_cols(name: str, t: torch.Tensor):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: a matrix is needed, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def checkpoint_exps_shape(rows: int, cols: int):
+    """Shape of the exponent bytes of a [rows, cols] checkpoint."""
+    return rows, (cols + 31) // 32
+
+
+def moe_lora_checkpoint_pack(x, codes, exps, stream=None) -> None:
+    """x [rows, cols] bf16 -> codes [rows, cols] and exps [rows, ceil(cols / 32)], uint8."""
+    M, H = _rows_cols("x", x)
+    _call("moe_lora_checkpoint_pack", _on(x, codes, exps), stream, M, H,
+          _checked("x", x, torch.bfloat16, M * H), _checked("codes", codes, torch.uint8, M * H),
+          _checked("exps", exps, torch.uint8, M * ((H + 31) // 32)))
+
+
+def moe_lora_checkpoint_unpack(codes, exps, x, stream=None) -> None:
+    M, H = _rows_cols("codes", codes)
+    _call("moe_lora_checkpoint_unpack", _on(codes, exps, x), stream, M, H,
+          _checked("codes", codes, torch.uint8, M * H), _checked("exps", exps, torch.uint8, M * ((H + 31) // 32)),
+          _checked("x", x, torch.bfloat16, M * H))
+
+
+def moe_lora_finalize_backward(d: Dims, d_out, topk_weights, e2p, d_y_perm, d_weights, y_perm=None, y_codes=None,
+                               y_exps=None, stream=None) -> None:
+    """y_perm in bf16, or its checkpoint (y_codes, y_exps)."""
+    T, H, R = d.num_tokens, d.hidden, d.num_tokens * d.top_k
+    _call("moe_lora_finalize_backward",
+          _on(d_out, topk_weights, e2p, d_y_perm, d_weights, y_perm, y_codes, y_exps), stream, ctypes.byref(d),
+          _checked("d_out", d_out, torch.bfloat16, T * H),
+          None if y_perm is None else _checked("y_perm", y_perm, torch.bfloat16, R * H),
+          None if y_codes is None else _checked("y_codes", y_codes, torch.uint8, R * H),
+          None if y_exps is None else _checked("y_exps", y_exps, torch.uint8, R * ((H + 31) // 32)),
+          _checked("topk_weights", topk_weights, torch.float32, R), _checked("e2p", e2p, torch.int32, R),
+          _checked("d_y_perm", d_y_perm, torch.bfloat16, R * H),
+          _checked("d_weights", d_weights, torch.float32, R))
+
+
 @dataclass
 class RouteOut:
     topk_ids: torch.Tensor

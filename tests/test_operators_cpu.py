@@ -115,3 +115,65 @@ def test_scored_gradient_equals_differences(score, renorm):
         diff = 1.5 * (dw * (ref.chosen_weights(up, ids, score, renorm) -
                             ref.chosen_weights(down, ids, score, renorm))).sum() / (2 * h)
         assert abs(diff - got[t, e]) < 1e-7
+
+
+# ---- checkpoints and finalize's gradients
+def test_checkpoint_refusals():
+    lib = pkg.load()
+    for fn in (lib.moe_lora_checkpoint_pack, lib.moe_lora_checkpoint_unpack):
+        assert fn(-1, 8, FAKE, FAKE, FAKE, None) == _lib.ERR_INVALID_ARGUMENT
+        assert fn(4, 0, FAKE, FAKE, FAKE, None) == _lib.ERR_INVALID_ARGUMENT
+        assert fn(4, 12, FAKE, FAKE, FAKE, None) == _lib.ERR_UNSUPPORTED
+        assert fn(4, 65544, FAKE, FAKE, FAKE, None) == _lib.ERR_UNSUPPORTED
+        assert fn(1 << 31, 8, FAKE, FAKE, FAKE, None) == _lib.ERR_UNSUPPORTED
+        assert fn(0, 8, None, None, None, None) == _lib.OK
+        for i in range(3):
+            args = [FAKE] * 3
+            args[i] = FAKE + 8
+            assert fn(4, 8, *args, None) == _lib.ERR_INVALID_ARGUMENT
+
+
+def test_finalize_backward_refusals():
+    lib = pkg.load()
+    d = _lib.Dims(4, 64, 8, 8, 2)
+
+    def call(dd=d, d_out=FAKE, y=FAKE, c=None, e=None, w=FAKE, e2p=FAKE, dy=FAKE, dw=FAKE):
+        return lib.moe_lora_finalize_backward(ctypes.byref(dd), d_out, y, c, e, w, e2p, dy, dw, None)
+
+    for bad in (dict(y=None), dict(c=FAKE), dict(c=FAKE, e=FAKE), dict(y=None, c=FAKE), dict(y=None, e=FAKE),
+                dict(d_out=None), dict(w=None), dict(e2p=FAKE + 4), dict(dy=None), dict(dw=None)):
+        assert call(**bad) == _lib.ERR_INVALID_ARGUMENT
+    assert call(dd=_lib.Dims(4, 60, 8, 8, 2)) == _lib.ERR_UNSUPPORTED
+    assert call(dd=_lib.Dims(0, 64, 8, 8, 2), d_out=None, y=None) == _lib.OK
+
+
+def test_checkpoint_oracle_on_hand_made_blocks():
+    x = np.zeros((1, 64))
+    x[0, 0], x[0, 1], x[0, 2] = 448.0, 17.0, -1.0    # exponent 0: 17 is a tie of 16 and 18, taken to even
+    x[0, 32], x[0, 33] = 450.0, 1.0                  # just past 448: exponent 1
+    codes, exps = ref.checkpoint_pack(x)
+    assert list(exps[0]) == [127, 128]
+    got = ref.checkpoint_unpack(codes, exps)[0]
+    assert list(got[:3]) == [448.0, 16.0, -1.0] and list(got[32:34]) == [448.0, 1.0]
+    assert ref.checkpoint_exponent(0.0) == -117 and ref.checkpoint_exponent(1.75) == -8
+
+
+def test_finalize_gradient_oracle_equals_differences():
+    g = np.random.Generator(np.random.PCG64(0))
+    T, k, H = 3, 2, 5
+    y, w, d_out = g.standard_normal((T * k, H)), g.random((T, k)), g.standard_normal((T, H))
+    e2p = g.permutation(T * k)
+
+    def loss(y, w):
+        return sum((w[t, j] * y[e2p[t * k + j]] * d_out[t]).sum() for t in range(T) for j in range(k))
+
+    dy, dw = ref.finalize_backward(d_out, y, w, e2p)
+    h = 1e-6
+    for p, i in itertools.product(range(T * k), range(H)):
+        e = np.zeros_like(y)
+        e[p, i] = h
+        assert abs((loss(y + e, w) - loss(y - e, w)) / (2 * h) - dy[p, i]) < 1e-8
+    for t, j in itertools.product(range(T), range(k)):
+        e = np.zeros_like(w)
+        e[t, j] = h
+        assert abs((loss(y, w + e) - loss(y, w - e)) / (2 * h) - dw[t, j]) < 1e-8
