@@ -384,6 +384,47 @@ int moe_lora_finalize_backward(const moe_lora_dims *dims, const uint16_t *d_out,
                                const int32_t *expanded_to_permuted, uint16_t *d_y_perm,
                                float *d_weights, moe_lora_stream_t stream);
 
+/* ---------------------------------------------------------------- projection, pooled adapters
+ * A dense projection that all requests share, with the low-rank adapter of each token's
+ * request beside it (the layers around the experts: attention projections, a shared
+ * expert), for many resident adapters:
+ *   a = token_slot[t];  v[t] = A[a] x[t];  y[t] = W x[t] + [a valid] scaling[a] * B[a] v[t]
+ * bf16 matrices, fp32 sums; scaling * v is rounded to bf16 once before the second product
+ * (as in the expert layer), y once.
+ *   x [T, in] rows ldx apart, w [out, in], y [T, out] rows ldy apart (columns between are
+ *   left as they were), v [T, max_rank] fp32: A x unscaled, zero past a row's rank; written
+ *   if not NULL (a backward pass takes it).
+ * in and out: multiples of 8, in * out < 2^30; ldx and ldy multiples of 8, at most 2^22 (else
+ * MOE_LORA_ERR_UNSUPPORTED).  T may be 0.  A token whose slot lies outside [0, num_slots), or
+ * whose adapter has rank 0, gets the shared projection alone.
+ * Workspace: moe_lora_project_workspace_size bytes, written before it is read; calls that
+ * may overlap need one each. */
+#define MOE_LORA_MAX_POOL_SLOTS 512
+#define MOE_LORA_MAX_POOL_RANK 128
+
+typedef struct {
+  int32_t num_tokens;   /* T >= 0 */
+  int32_t in_features;
+  int32_t out_features;
+  int32_t ldx;          /* elements between rows of x, >= in_features */
+  int32_t ldy;          /* elements between rows of y (or dy), >= out_features */
+} moe_lora_proj_dims;
+
+typedef struct {
+  int32_t num_slots;         /* 0..MOE_LORA_MAX_POOL_SLOTS; 0 = the shared projection alone */
+  int32_t max_rank;          /* ranks held per adapter: a multiple of 8, 8..MOE_LORA_MAX_POOL_RANK */
+  const int32_t *token_slot; /* [T] */
+  const int32_t *rank;       /* [num_slots], device; taken as within [0, max_rank] */
+  const float *scaling;      /* [num_slots], device */
+  const uint16_t *a;         /* [num_slots, max_rank, in]: rows past a slot's rank are not used */
+  const uint16_t *b;         /* [num_slots, out, max_rank]: columns past it are not used */
+} moe_lora_pool;
+
+size_t moe_lora_project_workspace_size(const moe_lora_proj_dims *dims, const moe_lora_pool *pool);
+int moe_lora_project(const moe_lora_proj_dims *dims, const uint16_t *x, const uint16_t *w,
+                     const moe_lora_pool *pool, uint16_t *y, float *v, void *ws, size_t ws_bytes,
+                     moe_lora_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

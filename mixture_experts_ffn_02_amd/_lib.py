@@ -54,6 +54,8 @@ EXPORTED = (
     "moe_lora_finalize_backward",
     "moe_lora_checkpoint_pack",
     "moe_lora_checkpoint_unpack",
+    "moe_lora_project_workspace_size",
+    "moe_lora_project",
 )
 
 
@@ -71,6 +73,16 @@ class ScoringC(ctypes.Structure):
     _fields_ = [("score", c_int32), ("logits_dtype", c_int32), ("renormalize", c_int32),
                 ("n_group", c_int32), ("topk_group", c_int32), ("group_score", c_int32),
                 ("scale", c_float), ("bias", c_void_p)]
+
+
+class ProjDims(ctypes.Structure):
+    _fields_ = [("num_tokens", c_int32), ("in_features", c_int32), ("out_features", c_int32),
+                ("ldx", c_int32), ("ldy", c_int32)]
+
+
+class Pool(ctypes.Structure):
+    _fields_ = [("num_slots", c_int32), ("max_rank", c_int32), ("token_slot", c_void_p),
+                ("rank", c_void_p), ("scaling", c_void_p), ("a", c_void_p), ("b", c_void_p)]
 
 
 class Adapters(ctypes.Structure):
@@ -159,6 +171,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     for name in ("moe_lora_checkpoint_pack", "moe_lora_checkpoint_unpack"):
         getattr(lib, name).restype = c_int
         getattr(lib, name).argtypes = [c_int64, c_int32, c_void_p, c_void_p, c_void_p, c_void_p]
+    lib.moe_lora_project_workspace_size.restype = c_size_t
+    lib.moe_lora_project_workspace_size.argtypes = [POINTER(ProjDims), POINTER(Pool)]
+    lib.moe_lora_project.restype = c_int
+    lib.moe_lora_project.argtypes = [POINTER(ProjDims), c_void_p, c_void_p, POINTER(Pool), c_void_p, c_void_p,
+                                     c_void_p, c_size_t, c_void_p]
     _lib = lib
     return lib
 

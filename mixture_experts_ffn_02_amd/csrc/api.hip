@@ -438,4 +438,56 @@ int moe_lora_finalize_backward(const moe_lora_dims *d, const uint16_t *d_out, co
   return moe::launch_finalize_backward(a, reinterpret_cast<hipStream_t>(stream));
 }
 
+namespace {
+
+int check_proj(const moe_lora_proj_dims *d, const moe_lora_pool *p, bool shape_only) {
+  if (!d) return MOE_LORA_ERR_INVALID_ARGUMENT;
+  if (d->num_tokens < 0 || d->in_features <= 0 || d->out_features <= 0 || d->ldx < d->in_features ||
+      d->ldy < d->out_features)
+    return MOE_LORA_ERR_INVALID_ARGUMENT;
+  if (d->in_features % 8 != 0 || d->out_features % 8 != 0 || d->ldx % 8 != 0 || d->ldy % 8 != 0 ||
+      d->ldx > (1 << 22) || d->ldy > (1 << 22) || (long long)d->in_features * d->out_features >= (1ll << 30))
+    return MOE_LORA_ERR_UNSUPPORTED;
+  if (!p) return MOE_LORA_ERR_INVALID_ARGUMENT;
+  if (p->num_slots < 0) return MOE_LORA_ERR_INVALID_ARGUMENT;
+  if (p->num_slots > MOE_LORA_MAX_POOL_SLOTS) return MOE_LORA_ERR_UNSUPPORTED;
+  if (p->num_slots > 0) {
+    if (p->max_rank <= 0) return MOE_LORA_ERR_INVALID_ARGUMENT;
+    if (p->max_rank % 8 != 0 || p->max_rank > MOE_LORA_MAX_POOL_RANK) return MOE_LORA_ERR_UNSUPPORTED;
+    if (!shape_only &&
+        (!p->token_slot || !p->rank || !p->scaling || !p->a || !p->b || !aligned16(p->token_slot) ||
+         !aligned16(p->rank) || !aligned16(p->scaling) || !aligned16(p->a) || !aligned16(p->b)))
+      return MOE_LORA_ERR_INVALID_ARGUMENT;
+  }
+  return MOE_LORA_OK;
+}
+
+moe::PoolView pool_view(const moe_lora_pool *p) {
+  return moe::PoolView{p->num_slots, p->num_slots > 0 ? p->max_rank : 8, p->token_slot, p->rank, p->scaling};
+}
+
+}  // namespace
+
+size_t moe_lora_project_workspace_size(const moe_lora_proj_dims *d, const moe_lora_pool *p) {
+  if (check_proj(d, p, true) != MOE_LORA_OK || d->num_tokens == 0 || p->num_slots == 0) return 0;
+  return moe::project_workspace_bytes(d->num_tokens, p->max_rank);
+}
+
+int moe_lora_project(const moe_lora_proj_dims *d, const uint16_t *x, const uint16_t *w, const moe_lora_pool *p,
+                     uint16_t *y, float *v, void *ws, size_t ws_bytes, moe_lora_stream_t stream) {
+  const int st = check_proj(d, p, d && d->num_tokens == 0);
+  if (st != MOE_LORA_OK) return st;
+  if (d->num_tokens == 0) return MOE_LORA_OK;
+  if (!x || !w || !y || !aligned16(x) || !aligned16(w) || !aligned16(y) || !aligned16(v))
+    return MOE_LORA_ERR_INVALID_ARGUMENT;
+  if (v && p->num_slots == 0) return MOE_LORA_ERR_INVALID_ARGUMENT;  // no adapter: no v
+  const size_t need = moe_lora_project_workspace_size(d, p);
+  if (ws_bytes < need) return MOE_LORA_ERR_WORKSPACE_TOO_SMALL;
+  if (need > 0 && (!ws || !aligned16(ws))) return MOE_LORA_ERR_INVALID_ARGUMENT;
+  const moe::ProjectArgs a{x,    d->ldx, d->num_tokens, d->in_features, d->out_features,
+                           w,    pool_view(p), p->a,    static_cast<const uint16_t *>(ws),
+                           p->b, y,      d->ldy};
+  return moe::launch_project(a, v, reinterpret_cast<hipStream_t>(stream));
+}
+
 }  // extern "C"

@@ -78,6 +78,35 @@ int launch_checkpoint_pack(long long rows, int cols, const uint16_t *x, uint8_t 
 int launch_checkpoint_unpack(long long rows, int cols, const uint8_t *codes, const uint8_t *exps, uint16_t *x,
                              hipStream_t s);
 
+// ---- projection with pooled adapters ------------------------------------------------
+struct PoolView {
+  int S, R;                   // adapters, ranks held for each
+  const int32_t *token_slot;  // [T]
+  const int32_t *rank;        // [S]
+  const float *scaling;       // [S]
+};
+struct ShrinkArgs {
+  const uint16_t *x;  // [T, K], rows ldx apart
+  int ldx, T, K;
+  const uint16_t *m;  // A [S, R, K], or B [S, K, R]
+  PoolView pool;
+  uint16_t *out_bf16;  // [T, R]
+  float *out_f32;      // [T, R] or NULL
+};
+struct ProjectArgs {
+  const uint16_t *x;  // [T, K], rows ldx apart
+  int ldx, T, K, N;
+  const uint16_t *w;
+  PoolView pool;
+  const uint16_t *a_or_b;  // the shrink's matrices
+  const uint16_t *ext_a;   // bf16 [T, R], the shrink's result
+  const uint16_t *ext_b;   // the expand's matrices
+  uint16_t *y;
+  int ldy;
+};
+size_t project_workspace_bytes(int T, int R);
+int launch_project(const ProjectArgs &a, float *v, hipStream_t s);
+
 // ---- tile-packed expert weights ---------------------------------------------------
 int launch_pack_weights_fp8(const moe_lora_dims &d, const uint8_t *w1, const uint8_t *w2, uint8_t *w1p,
                             uint8_t *w2p, hipStream_t s);

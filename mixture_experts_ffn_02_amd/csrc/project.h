@@ -1,0 +1,102 @@
+// Shared pieces of the pooled-adapter projection kernels (gfx950).
+#pragma once
+
+#include "common.h"
+#include "kernels.h"
+
+namespace moe {
+
+// 16 zero bytes for lanes whose chunk lies outside its matrix (a masked lane still reads)
+__device__ __attribute__((aligned(16))) static const uint32_t kZeroChunk[4] = {0u, 0u, 0u, 0u};
+
+// One 16-byte chunk per lane from global memory straight into LDS: lane l writes LDS bytes
+// [lds + 16 l, lds + 16 l + 16).  Counts in vmcnt like any load; nothing waits here.
+MOE_DEV void dma16(const void *src, uint32_t lds) {
+  uint32_t saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %2\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, off\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "v"(src), "s"(lds)
+      : "memory");
+}
+// the same with a wave-uniform base and a 32-bit byte offset per lane
+MOE_DEV void dma16(const void *base, uint32_t off, uint32_t lds) {
+  uint32_t saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %3\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, %2\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "v"(off), "s"(base), "s"(lds)
+      : "memory");
+}
+MOE_DEV void dma_wait_all() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+MOE_DEV uint32_t lds_byte(const void *p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void *)p));
+}
+
+// Transposed LDS read: each group of 16 lanes reads a 4 x 16 block of 16-bit values, lane i
+// giving the address of row i / 4, columns 4 (i % 4) .. + 3; it receives column i's 4 rows.
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+MOE_DEV u32x2_t lds_read_tr(const uint16_t *p) {
+  return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                         (__attribute__((address_space(3))) s16x4_t *)p));
+}
+
+// orders one wavefront's own LDS writes and reads
+MOE_DEV void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// slot of a token with an adapter of positive rank, else -1; its rank
+MOE_DEV int adapter_of(const PoolView &P, int t, int &rank) {
+  const int s = P.token_slot[t];
+  rank = 0;
+  if (s < 0 || s >= P.S) return -1;
+  const int r = P.rank[s];
+  rank = r < P.R ? r : P.R;
+  return rank > 0 ? s : -1;
+}
+MOE_DEV int rank_of(const PoolView &P, int s) {
+  const int r = P.rank[s];
+  return r < P.R ? r : P.R;
+}
+
+// Distinct adapters of a tile's rows: row slots into s_slot, the ascending list into s_list,
+// its length returned (uniform).  Called by the whole workgroup; s_bits: 16 words.
+template <int ROWS, int NT>
+MOE_DEV int tile_adapters(const PoolView &P, int t0, int T, int *s_slot, int *s_list, uint32_t *s_bits) {
+  const int tid = threadIdx.x;
+  if (tid < 16) s_bits[tid] = 0u;
+  __syncthreads();
+  for (int r = tid; r < ROWS; r += NT) {
+    int s = -1, rank;
+    if (P.S > 0 && t0 + r < T) s = adapter_of(P, t0 + r, rank);
+    s_slot[r] = s;
+    if (s >= 0) atomicOr(&s_bits[s >> 5], 1u << (s & 31));
+  }
+  __syncthreads();
+  int n = 0;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) n += __popc(s_bits[w]);
+  for (int s = tid; s < 512; s += NT) {
+    if ((s_bits[s >> 5] >> (s & 31)) & 1u) {
+      int at = __popc(s_bits[s >> 5] & ((1u << (s & 31)) - 1u));
+      for (int w = 0; w < (s >> 5); ++w) at += __popc(s_bits[w]);
+      s_list[at] = s;
+    }
+  }
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(n);
+}
+
+}  // namespace moe

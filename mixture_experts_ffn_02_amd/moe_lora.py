@@ -291,6 +291,68 @@ def moe_lora_finalize_backward(d: Dims, d_out, topk_weights, e2p, d_y_perm, d_we
 
 
 @dataclass
+class AdapterPool:
+    """Resident adapters of a projection (device tensors): a [S, R, in] and b [S, out, R] bf16,
+    rank [S] int32 and scaling [S] fp32; token_slot [T] int32 names each token's adapter
+    (outside [0, S): none)."""
+
+    token_slot: torch.Tensor
+    rank: torch.Tensor
+    scaling: torch.Tensor
+    a: torch.Tensor
+    b: torch.Tensor
+
+    def to_c(self, T: int, K: int, N: int) -> _lib.Pool:
+        if self.a.dim() != 3 or self.b.dim() != 3:
+            raise ValueError("a is [S, R, in] and b [S, out, R]")
+        S, R = self.a.shape[0], self.a.shape[1]
+        bf16 = torch.bfloat16
+        return _lib.Pool(S, R, _checked("token_slot", self.token_slot, torch.int32, T),
+                         _checked("rank", self.rank, torch.int32, S),
+                         _checked("scaling", self.scaling, torch.float32, S),
+                         _checked("a", self.a, bf16, S * R * K), _checked("b", self.b, bf16, S * N * R))
+
+
+def _matrix(name: str, t: torch.Tensor, cols: int) -> int:
+    """Pointer of a bf16 matrix [*, cols] whose rows may lie apart (unit stride along them)."""
+    if t.dtype is not torch.bfloat16 and t.dtype not in (torch.int16, torch.uint16):
+        raise ValueError(f"{name}: torch.bfloat16 expected, got {t.dtype}")
+    if t.dim() != 2 or t.shape[1] != cols:
+        raise ValueError(f"{name}: [T, {cols}] expected, got shape {tuple(t.shape)}")
+    if t.shape[0] > 0 and (t.stride(1) != 1 or (t.shape[0] > 1 and t.stride(0) < cols)):
+        raise ValueError(f"{name}: rows must have unit stride and not overlap")
+    return t.data_ptr()
+
+
+def _pitch(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _proj_dims(T: int, K: int, N: int, x=None, y=None) -> _lib.ProjDims:
+    return _lib.ProjDims(T, K, N, K if x is None else _pitch(x), N if y is None else _pitch(y))
+
+
+def moe_lora_project_workspace_size(T: int, K: int, N: int, pool: AdapterPool) -> int:
+    p = pool.to_c(T, K, N)
+    return int(load().moe_lora_project_workspace_size(ctypes.byref(_proj_dims(T, K, N)), ctypes.byref(p)))
+
+
+def moe_lora_project(x, w, pool: AdapterPool, y, ws, v=None, stream=None) -> None:
+    """y = x W^T + scaling * (x A^T) B^T with each token's adapter; v [T, R] fp32 keeps x A^T.
+    x and y may be column slices of wider matrices."""
+    T, K = _rows_cols("x", x)
+    N = w.shape[0]
+    p = pool.to_c(T, K, N)
+    if y.shape[0] != T:
+        raise ValueError(f"y: {T} rows expected, got {y.shape[0]}")
+    _call("moe_lora_project", _on(x, w, y, ws, v, pool.token_slot, pool.rank, pool.scaling, pool.a, pool.b), stream,
+          ctypes.byref(_proj_dims(T, K, N, x, y)), _matrix("x", x, K), _checked("w", w, torch.bfloat16, N * K),
+          ctypes.byref(p), _matrix("y", y, N),
+          None if v is None else _checked("v", v, torch.float32, T * pool.a.shape[1]),
+          _ptr(ws), ws.numel() * ws.element_size() if ws is not None else 0)
+
+
+@dataclass
 class RouteOut:
     topk_ids: torch.Tensor
     topk_weights: torch.Tensor

@@ -177,3 +177,62 @@ def test_finalize_gradient_oracle_equals_differences():
         e = np.zeros_like(w)
         e[t, j] = h
         assert abs((loss(y, w + e) - loss(y, w - e)) / (2 * h) - dw[t, j]) < 1e-8
+
+
+# ---- projection with pooled adapters
+def _pool(**kw):
+    v = dict(num_slots=2, max_rank=16, token_slot=FAKE, rank=FAKE, scaling=FAKE, a=FAKE, b=FAKE)
+    v.update(kw)
+    return _lib.Pool(*[v[f] for f, _ in _lib.Pool._fields_])
+
+
+def _project(d, p, x=FAKE, w=FAKE, y=FAKE, v=None, ws=FAKE, ws_bytes=1 << 20):
+    return pkg.load().moe_lora_project(ctypes.byref(d), x, w, ctypes.byref(p) if p else None, y, v, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("dims,status", [
+    ((-1, 64, 48, 64, 48), _lib.ERR_INVALID_ARGUMENT), ((4, 0, 48, 64, 48), _lib.ERR_INVALID_ARGUMENT),
+    ((4, 64, 48, 56, 48), _lib.ERR_INVALID_ARGUMENT), ((4, 64, 48, 64, 40), _lib.ERR_INVALID_ARGUMENT),
+    ((4, 60, 48, 64, 48), _lib.ERR_UNSUPPORTED), ((4, 64, 44, 64, 48), _lib.ERR_UNSUPPORTED),
+    ((4, 64, 48, 68, 48), _lib.ERR_UNSUPPORTED), ((4, 64, 48, 64, 1 << 23), _lib.ERR_UNSUPPORTED),
+    ((4, 32768, 32768, 32768, 32768), _lib.ERR_UNSUPPORTED)])
+def test_project_refuses_bad_sizes(dims, status):
+    d = _lib.ProjDims(*dims)
+    assert _project(d, _pool()) == status
+    assert pkg.load().moe_lora_project_workspace_size(ctypes.byref(d), ctypes.byref(_pool())) == 0
+
+
+def test_project_refuses_bad_pools_and_pointers():
+    d = _lib.ProjDims(4, 64, 48, 64, 48)
+    bad, no = _lib.ERR_INVALID_ARGUMENT, _lib.ERR_UNSUPPORTED
+    assert _project(d, None) == bad
+    assert _project(d, _pool(num_slots=-1)) == bad
+    assert _project(d, _pool(num_slots=513)) == no
+    assert _project(d, _pool(max_rank=0)) == bad
+    assert _project(d, _pool(max_rank=12)) == no
+    assert _project(d, _pool(max_rank=136)) == no
+    for f in ("token_slot", "rank", "scaling", "a", "b"):
+        assert _project(d, _pool(**{f: None})) == bad
+        assert _project(d, _pool(**{f: FAKE + 4})) == bad
+    for f in ("x", "w", "y"):
+        assert _project(d, _pool(), **{f: None}) == bad
+        assert _project(d, _pool(), **{f: FAKE + 8}) == bad
+    assert _project(d, _pool(), v=FAKE + 4) == bad
+    assert _project(d, _pool(num_slots=0), v=FAKE) == bad
+    assert _project(d, _pool(), ws_bytes=8) == _lib.ERR_WORKSPACE_TOO_SMALL
+    assert _project(d, _pool(), ws=None) == bad
+    assert _project(_lib.ProjDims(0, 64, 48, 64, 48), _pool(), x=None, w=None, y=None, ws=None, ws_bytes=0) == _lib.OK
+
+
+def test_project_oracle_is_the_merged_weight():
+    g = np.random.Generator(np.random.PCG64(0))
+    T, K, N, S, R = 6, 5, 4, 3, 3
+    x, w, a, b = (g.standard_normal(s) for s in ((T, K), (N, K), (S, R, K), (S, N, R)))
+    slot, rank, scaling = np.array([0, 1, 2, -1, 3, 0]), np.array([3, 2, 0]), np.array([0.5, 2.0, 1.0])
+    y, v = ref.project(x, w, slot, rank, scaling, a, b)
+    for t in range(T):
+        m, s = w.copy(), slot[t]
+        if 0 <= s < S:
+            m += scaling[s] * b[s][:, :rank[s]] @ a[s][:rank[s]]
+        np.testing.assert_allclose(y[t], m @ x[t], rtol=1e-12)
+    assert (v[2:5] == 0).all() and (v[1, 2:] == 0).all()
