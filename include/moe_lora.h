@@ -425,6 +425,24 @@ int moe_lora_project(const moe_lora_proj_dims *dims, const uint16_t *x, const ui
                      const moe_lora_pool *pool, uint16_t *y, float *v, void *ws, size_t ws_bytes,
                      moe_lora_stream_t stream);
 
+/* Gradients for dy [T, out] (rows dims->ldy apart) with W frozen, over a = token_slot[t]:
+ *   u[t] = scaling[a] * B[a]^T dy[t]
+ *   dx[t] = W^T dy[t] + A[a]^T u[t]                               [T, in], rows in apart
+ *   da[s] = sum over the tokens of s of u[t] x[t]^T               [num_slots, max_rank, in]
+ *   db[s] = scaling[s] * sum over them of dy[t] v[t]^T            [num_slots, out, max_rank]
+ * all bf16, sums in fp32 (u enters dx rounded to bf16, da and db with 16 bits), every element
+ * written: zeros for adapters without tokens and past an adapter's rank.  Repeated calls
+ * give the same bits.  dx, da and db may each be NULL (not wanted; not all three).
+ *   x: the forward's input in bf16 (rows dims->ldx apart), or its 8-bit checkpoint (x_codes,
+ *   x_exps, x NULL); for da only.  w: for dx only.  v: the forward's v; for db only.
+ * Giving both forms of x, or neither with da, is MOE_LORA_ERR_INVALID_ARGUMENT.
+ * Workspace: moe_lora_project_backward_workspace_size bytes, as above. */
+size_t moe_lora_project_backward_workspace_size(const moe_lora_proj_dims *dims, const moe_lora_pool *pool);
+int moe_lora_project_backward(const moe_lora_proj_dims *dims, const uint16_t *x, const uint8_t *x_codes,
+                              const uint8_t *x_exps, const uint16_t *w, const moe_lora_pool *pool,
+                              const float *v, const uint16_t *dy, uint16_t *dx, uint16_t *da, uint16_t *db,
+                              void *ws, size_t ws_bytes, moe_lora_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

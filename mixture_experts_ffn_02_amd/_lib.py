@@ -56,6 +56,8 @@ EXPORTED = (
     "moe_lora_checkpoint_unpack",
     "moe_lora_project_workspace_size",
     "moe_lora_project",
+    "moe_lora_project_backward_workspace_size",
+    "moe_lora_project_backward",
 )
 
 
@@ -176,6 +178,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_lora_project.restype = c_int
     lib.moe_lora_project.argtypes = [POINTER(ProjDims), c_void_p, c_void_p, POINTER(Pool), c_void_p, c_void_p,
                                      c_void_p, c_size_t, c_void_p]
+    lib.moe_lora_project_backward_workspace_size.restype = c_size_t
+    lib.moe_lora_project_backward_workspace_size.argtypes = [POINTER(ProjDims), POINTER(Pool)]
+    lib.moe_lora_project_backward.restype = c_int
+    lib.moe_lora_project_backward.argtypes = ([POINTER(ProjDims)] + [c_void_p] * 4 + [POINTER(Pool)] +
+                                              [c_void_p] * 6 + [c_size_t, c_void_p])
     _lib = lib
     return lib
 

@@ -490,4 +490,41 @@ int moe_lora_project(const moe_lora_proj_dims *d, const uint16_t *x, const uint1
   return moe::launch_project(a, v, reinterpret_cast<hipStream_t>(stream));
 }
 
+size_t moe_lora_project_backward_workspace_size(const moe_lora_proj_dims *d, const moe_lora_pool *p) {
+  if (check_proj(d, p, true) != MOE_LORA_OK || d->num_tokens == 0 || p->num_slots == 0) return 0;
+  return moe::project_backward_workspace_bytes(d->num_tokens, d->in_features, d->out_features, p->num_slots,
+                                               p->max_rank);
+}
+
+int moe_lora_project_backward(const moe_lora_proj_dims *d, const uint16_t *x, const uint8_t *x_codes,
+                              const uint8_t *x_exps, const uint16_t *w, const moe_lora_pool *p, const float *v,
+                              const uint16_t *dy, uint16_t *dx, uint16_t *da, uint16_t *db, void *ws,
+                              size_t ws_bytes, moe_lora_stream_t stream) {
+  const int st = check_proj(d, p, d && d->num_tokens == 0);
+  if (st != MOE_LORA_OK) return st;
+  if (!dx && !da && !db) return MOE_LORA_ERR_INVALID_ARGUMENT;
+  if (!aligned16(dx) || !aligned16(da) || !aligned16(db)) return MOE_LORA_ERR_INVALID_ARGUMENT;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (d->num_tokens == 0) {  // the adapters' gradients are sums over nothing
+    const size_t n = (size_t)p->num_slots * p->max_rank;
+    if (da && n > 0 && moe::launch_zero16(da, n * d->in_features, s) != ST_OK) return MOE_LORA_ERR_HIP;
+    if (db && n > 0 && moe::launch_zero16(db, n * d->out_features, s) != ST_OK) return MOE_LORA_ERR_HIP;
+    return MOE_LORA_OK;
+  }
+  if (!dy || !aligned16(dy) || !aligned16(x) || !aligned16(x_codes) || !aligned16(x_exps) || !aligned16(w) ||
+      !aligned16(v))
+    return MOE_LORA_ERR_INVALID_ARGUMENT;
+  const bool codes = x_codes || x_exps;
+  if (codes && (x || !x_codes || !x_exps)) return MOE_LORA_ERR_INVALID_ARGUMENT;
+  if (p->num_slots > 0 && ((da && !x && !codes) || (db && !v))) return MOE_LORA_ERR_INVALID_ARGUMENT;
+  if (dx && !w) return MOE_LORA_ERR_INVALID_ARGUMENT;
+  const size_t need = moe_lora_project_backward_workspace_size(d, p);
+  if (ws_bytes < need) return MOE_LORA_ERR_WORKSPACE_TOO_SMALL;
+  if (need > 0 && (!ws || !aligned16(ws))) return MOE_LORA_ERR_INVALID_ARGUMENT;
+  const moe::ProjectBackwardArgs a{x,    d->ldx, x_codes, x_exps, dy,           d->ldy, d->num_tokens, d->in_features,
+                                   d->out_features, w,    p->a,    p->b,   pool_view(p), v,      dx,            da,
+                                   db,   ws};
+  return moe::launch_project_backward(a, s);
+}
+
 }  // extern "C"

@@ -105,6 +105,38 @@ struct ProjectArgs {
   int ldy;
 };
 size_t project_workspace_bytes(int T, int R);
+// the shrink over B [S, K, R] and the product with w [K, N], ext_b [S, R, N]
+int launch_shrink_transposed(const ShrinkArgs &a, hipStream_t s);
+int launch_product_transposed(const ProjectArgs &a, hipStream_t s);
+
+struct AdapterGradArgs {
+  const uint16_t *x;  // [T, K], rows ldx apart, or NULL with the checkpoint
+  int ldx;
+  const uint8_t *codes, *exps;  // [T, K], [T, ceil(K / 32)]
+  const uint16_t *dy;           // [T, N], rows ldy apart
+  int ldy, K, N;
+  const float *u, *v;  // [T, R]
+  PoolView pool;
+  const int32_t *order, *seg;
+  uint16_t *da, *db;  // [S, R, K], [S, N, R]; either may be NULL
+  float *part_a, *part_b;
+  int parts, tiles_a;
+};
+struct ProjectBackwardArgs {
+  const uint16_t *x;
+  int ldx;
+  const uint8_t *codes, *exps;
+  const uint16_t *dy;
+  int ldy, T, K, N;
+  const uint16_t *w, *a, *b;
+  PoolView pool;
+  const float *v;
+  uint16_t *dx, *da, *db;
+  void *ws;
+};
+size_t project_backward_workspace_bytes(int T, int K, int N, int S, int R);
+int launch_zero16(uint16_t *p, size_t n, hipStream_t s);
+int launch_project_backward(const ProjectBackwardArgs &a, hipStream_t s);
 int launch_project(const ProjectArgs &a, float *v, hipStream_t s);
 
 // ---- tile-packed expert weights ---------------------------------------------------

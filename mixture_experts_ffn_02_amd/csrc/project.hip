@@ -298,6 +298,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void project_tile_kernel(const Proj
   constexpr int WTM = BM / WM, WTN = BN / WN, FM = WTM / 16, FN = WTN / 16;
   constexpr int A_IT = BM * 8 / NT, B_IT = BN * 8 / NT;
   constexpr int BCH = BN / 8;  // chunks per row of B (NN)
+  constexpr int SWZ = BN / 16 < 8 ? BN / 16 - 1 : 7;  // its pairs' swizzle stays inside a row
   __shared__ __attribute__((aligned(16))) uint16_t As[2][BM * 64];
   __shared__ __attribute__((aligned(16))) uint16_t Bs[2][BN * 64];
   __shared__ int s_slot[BM], s_list[BM];
@@ -337,7 +338,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void project_tile_kernel(const Proj
       b_k[i] = c * 8;
       b_off[i] = ((uint32_t)min(r, N - 1 - n0) * (uint32_t)K + c * 8) * 2u;
     } else {
-      const int r = q / BCH, c = (q % BCH) ^ (((r & 3) | ((r >> 1) & 4)) << 1);
+      const int r = q / BCH, c = (q % BCH) ^ ((((r & 3) | ((r >> 1) & 4)) & SWZ) << 1);
       b_k[i] = r;
       b_off[i] = ((uint32_t)r * (uint32_t)N + (uint32_t)min(c * 8, N - 8 - n0)) * 2u;
     }
@@ -383,7 +384,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void project_tile_kernel(const Proj
         if (r0 + b_k[i] < rank && n < N)
           src = reinterpret_cast<const char *>(P.ext_b + ((size_t)slot * N + n) * pool.R + r0 + b_k[i]);
       } else {
-        const int q = i * NT + tid, c = (q % BCH) ^ (((b_k[i] & 3) | ((b_k[i] >> 1) & 4)) << 1);
+        const int q = i * NT + tid, c = (q % BCH) ^ ((((b_k[i] & 3) | ((b_k[i] >> 1) & 4)) & SWZ) << 1);
         if (r0 + b_k[i] < rank && n0 + c * 8 < N)
           src = reinterpret_cast<const char *>(P.ext_b + ((size_t)slot * pool.R + r0 + b_k[i]) * N + n0 + c * 8);
       }
@@ -405,7 +406,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void project_tile_kernel(const Proj
   }
   // NN: lane's row of a transposed read is 32 kk + 8 grp + row / 4 (+ 4), whose swizzle is
   // (row / 4) | 4 (grp & 1); columns 4 (row % 4) of a 16-wide piece (one 32-byte pair)
-  const int tr_row = grp * 8 + (row >> 2), tr_swz = (row >> 2) | ((grp & 1) << 2);
+  const int tr_row = grp * 8 + (row >> 2), tr_swz = ((row >> 2) | ((grp & 1) << 2)) & SWZ;
 
   auto fragments = [&](int buf, int kk, u32x4_t(&af)[FM], u32x4_t(&bf)[FN]) {
 #pragma unroll
@@ -563,6 +564,9 @@ int launch_product(const ProjectArgs &a, hipStream_t s) {
 }
 
 }  // namespace
+
+int launch_shrink_transposed(const ShrinkArgs &a, hipStream_t s) { return launch_shrink<true>(a, s); }
+int launch_product_transposed(const ProjectArgs &a, hipStream_t s) { return launch_product<true>(a, s); }
 
 size_t project_workspace_bytes(int T, int R) { return ((size_t)T * R * 2 + 255) & ~(size_t)255; }
 

@@ -352,6 +352,35 @@ def moe_lora_project(x, w, pool: AdapterPool, y, ws, v=None, stream=None) -> Non
           _ptr(ws), ws.numel() * ws.element_size() if ws is not None else 0)
 
 
+def moe_lora_project_backward_workspace_size(T: int, K: int, N: int, pool: AdapterPool) -> int:
+    p = pool.to_c(T, K, N)
+    return int(load().moe_lora_project_backward_workspace_size(ctypes.byref(_proj_dims(T, K, N)), ctypes.byref(p)))
+
+
+def moe_lora_project_backward(dy, w, pool: AdapterPool, v, ws, x=None, x_codes=None, x_exps=None, dx=None, da=None,
+                              db=None, stream=None) -> None:
+    """Gradients of moe_lora_project: dx [T, in], da [S, R, in], db [S, out, R] (None: not
+    wanted).  The input is x in bf16 or its checkpoint (x_codes, x_exps); v the forward's."""
+    T, N = _rows_cols("dy", dy)
+    K = w.shape[1]
+    S, R = pool.a.shape[0], pool.a.shape[1]
+    p = pool.to_c(T, K, N)
+    bf16, u8 = torch.bfloat16, torch.uint8
+    if x is not None and x.shape[0] != T:
+        raise ValueError(f"x: {T} rows expected, got {x.shape[0]}")
+    _call("moe_lora_project_backward",
+          _on(dy, w, v, ws, x, x_codes, x_exps, dx, da, db, pool.token_slot, pool.rank, pool.scaling, pool.a, pool.b),
+          stream, ctypes.byref(_proj_dims(T, K, N, x, dy)), None if x is None else _matrix("x", x, K),
+          None if x_codes is None else _checked("x_codes", x_codes, u8, T * K),
+          None if x_exps is None else _checked("x_exps", x_exps, u8, T * ((K + 31) // 32)),
+          _checked("w", w, bf16, N * K), ctypes.byref(p),
+          None if v is None else _checked("v", v, torch.float32, T * R), _matrix("dy", dy, N),
+          None if dx is None else _checked("dx", dx, bf16, T * K),
+          None if da is None else _checked("da", da, bf16, S * R * K),
+          None if db is None else _checked("db", db, bf16, S * N * R),
+          _ptr(ws), ws.numel() * ws.element_size() if ws is not None else 0)
+
+
 @dataclass
 class RouteOut:
     topk_ids: torch.Tensor

@@ -61,6 +61,55 @@ class Case:
         assert (y[:, self.N:] == 7.0).all()
         return y[:, :self.N], v
 
+    def backward(self, codes=False, want=("dx", "da", "db"), pad=0, **kw):
+        T, K, N, S, R = self.T, self.K, self.N, self.S, self.R
+        g = np.random.Generator(np.random.PCG64(77))
+        self.dy = bf(g.standard_normal((T, N + pad)))[:, :N]
+        a, b = self.clean
+        if codes:
+            self.codes = torch.empty((T, K), dtype=torch.uint8, device=dev())
+            self.exps = torch.empty(ml.checkpoint_exps_shape(T, K), dtype=torch.uint8, device=dev())
+            ml.moe_lora_checkpoint_pack(self.x.contiguous(), self.codes, self.exps)
+            self.x64 = ref.checkpoint_unpack(self.codes.cpu().numpy(), self.exps.cpu().numpy())
+            src = dict(x_codes=self.codes, x_exps=self.exps)
+        else:
+            self.x64, src = f64(self.x), dict(x=self.x)
+        # v as a forward pass leaves it
+        self.v = torch.from_numpy(ref.project(f64(self.x), f64(self.w), self.slot, self.rank, self.scaling, a, b)[1]
+                                  .astype(np.float32)).to(dev())
+        nan = lambda *s: torch.full(s, float("nan"), dtype=torch.bfloat16, device=dev())  # noqa: E731
+        out = dict(dx=nan(T, K), da=nan(S, R, K), db=nan(S, N, R))
+        ws = torch.full((max(1, ml.moe_lora_project_backward_workspace_size(T, K, N, self.pool)),), 0xFF,
+                        dtype=torch.uint8, device=dev())
+        ml.moe_lora_project_backward(self.dy, self.w, self.pool, self.v, ws, **src, **{k: out[k] for k in want}, **kw)
+        torch.cuda.synchronize()
+        return out
+
+    def check_backward(self, out, want=("dx", "da", "db")):
+        a, b = self.clean
+        args = [f64(self.dy), self.x64, f64(self.w), self.slot, self.rank, self.scaling, a, b,
+                self.v.double().cpu().numpy()]
+        exact = dict(zip(("dx", "da", "db"), ref.project_backward(*args)))
+        absd = [np.abs(m) if m.dtype == np.float64 else m for m in args]
+        mag = dict(zip(("dx", "da", "db"), ref.project_backward(*absd)))
+        # the delta's share of dx: u is rounded to bf16 once
+        delta = ref.project_backward(args[0], *args[1:2], np.zeros_like(args[2]), *args[3:])[0]
+        u_abs = np.zeros_like(delta)
+        for s in range(self.S):
+            rows, r = np.flatnonzero(self.slot == s), min(max(self.rank[s], 0), self.R)
+            u = float(self.scaling[s]) * (args[0][rows] @ b[s, :, :r])
+            u_abs[rows] = np.abs(u) @ np.abs(a[s, :r])
+        fp32 = 2 * (max(self.N, self.T) + self.R + 16) * ULP
+        tol = dict(dx=HALF * np.abs(exact["dx"]) + 1.01 * HALF * u_abs + fp32 * mag["dx"])
+        # da and db: u and v enter as two bf16 terms, 2^-16 of each product at most, u itself
+        # an fp32 sum over N
+        for k in ("da", "db"):
+            tol[k] = HALF * np.abs(exact[k]) + (2.0 ** -16 + 2 * fp32) * mag[k]
+        for k in want:
+            err = np.abs(f64(out[k]) - exact[k])
+            assert np.isfinite(f64(out[k])).all(), k
+            assert (err <= tol[k]).all(), (k, float((err - tol[k]).max()))
+
     def check_forward(self, y, v):
         a, b = self.clean
         x, w = f64(self.x), f64(self.w)
@@ -97,6 +146,112 @@ def test_forward(T, K, N, S, R, pad):
     say(f"[project] T={T} K={K} N={N} S={S} R={R} pad={pad}")
     c = Case(T, K, N, S, R, pad=pad)
     c.check_forward(*c.forward(ldy_pad=pad))
+
+
+@pytest.mark.parametrize("codes", [False, True], ids=["bf16", "codes"])
+@pytest.mark.parametrize("T,K,N,S,R,pad", SHAPES)
+def test_backward(T, K, N, S, R, pad, codes):
+    say(f"[project backward] T={T} K={K} N={N} S={S} R={R} pad={pad} codes={codes}")
+    c = Case(T, K, N, S, R, pad=pad)
+    c.check_backward(c.backward(codes, pad=pad))
+
+
+@pytest.mark.parametrize("want", [("dx",), ("da",), ("db",), ("da", "db"), ("dx", "db")], ids="+".join)
+def test_backward_of_what_is_wanted(want):
+    c = Case(300, 128, 200, 3, 16)
+    out = c.backward(want=want)
+    c.check_backward(out, want)
+    for k in set(out) - set(want):
+        assert torch.isnan(out[k]).all()
+
+
+def test_backward_interleaved_and_split():
+    """Many adapters without order in a long batch, and one adapter whose tokens are split."""
+    c = Case(2100, 64, 136, 40, 16, mixed=True)
+    c.check_backward(c.backward())
+    c = Case(5000, 136, 72, 1, 16, mixed=False)
+    out = c.backward(codes=True)
+    c.check_backward(out)
+    again = c.backward(codes=True)
+    assert all(torch.equal(out[k], again[k]) for k in out)
+
+
+def test_backward_requests_do_not_reach_each_other():
+    c = Case(600, 128, 200, 4, 16, mixed=False, dirty=False)
+    out = {k: v.clone() for k, v in c.backward().items()}
+    victim = int(np.flatnonzero(c.slot == 3)[0])
+    c.x[victim], c.a[3] = float("nan"), float("inf")
+    c.clean[0][3] = 0  # (v is made from the clean matrices)
+    x = c.x.clone()
+    c.x[victim] = 0
+    v = c.backward()  # sets c.dy and c.v with finite values
+    c.x.copy_(x)
+    ws = torch.empty((ml.moe_lora_project_backward_workspace_size(600, 128, 200, c.pool),), dtype=torch.uint8, device=dev())
+    ml.moe_lora_project_backward(c.dy, c.w, c.pool, c.v, ws, x=c.x, **v)
+    keep = torch.from_numpy(c.slot != 3).to(dev())
+    assert torch.equal(v["dx"][keep], out["dx"][keep])
+    assert torch.equal(v["da"][:3], out["da"][:3]) and torch.equal(v["db"][:3], out["db"][:3])
+    assert torch.isnan(v["da"][3]).any()
+
+
+def test_backward_of_no_tokens_is_zero():
+    c = Case(8, 64, 48, 2, 16)
+    empty = ml.AdapterPool(c.pool.token_slot[:0], c.pool.rank, c.pool.scaling, c.a, c.b)
+    da, db = torch.full_like(c.a, 7.0), torch.full_like(c.b, 7.0)
+    ml.moe_lora_project_backward(c.forward()[0][:0], c.w, empty, None, None, x=c.x[:0], da=da, db=db)
+    assert (da == 0).all() and (db == 0).all()
+
+
+def test_training_step_of_the_adapters():
+    """Forward with v kept, the input into its checkpoint, backward from it: the gradients of the
+    loss sum(y * dy) against differences of the fp64 forward, eager and captured."""
+    c = Case(90, 64, 48, 3, 8, mixed=True, dirty=False)
+    g = np.random.Generator(np.random.PCG64(9))
+    dy = bf(g.standard_normal((90, 48)))
+    need = max(ml.moe_lora_project_workspace_size(90, 64, 48, c.pool),
+               ml.moe_lora_project_backward_workspace_size(90, 64, 48, c.pool))
+    ws = torch.empty((need,), dtype=torch.uint8, device=dev())
+    y, v = torch.empty_like(dy), torch.empty((90, 8), device=dev())
+    codes = torch.empty((90, 64), dtype=torch.uint8, device=dev())
+    exps = torch.empty((90, 2), dtype=torch.uint8, device=dev())
+    dx, da, db = torch.empty_like(c.x), torch.empty_like(c.a), torch.empty_like(c.b)
+
+    def step():
+        ml.moe_lora_project(c.x, c.w, c.pool, y, ws, v=v)
+        ml.moe_lora_checkpoint_pack(c.x, codes, exps)
+        ml.moe_lora_project_backward(dy, c.w, c.pool, v, ws, x_codes=codes, x_exps=exps, dx=dx, da=da, db=db)
+
+    step()
+    torch.cuda.synchronize()
+    eager = [t.clone() for t in (y, dx, da, db)]
+    # the checkpointed input moves da by its own rounding only: differences on its values
+    x8 = ref.checkpoint_unpack(codes.cpu().numpy(), exps.cpu().numpy())
+    a64, b64, w64, dy64 = f64(c.a), f64(c.b), f64(c.w), f64(dy)
+
+    def loss(x, a, b):
+        return (dy64 * ref.project(x, w64, c.slot, c.rank, c.scaling, a, b)[0]).sum()
+
+    h = 1e-4
+    for (name, got, base, x) in (("dx", dx, 0, f64(c.x)), ("da", da, 1, x8), ("db", db, 2, f64(c.x))):
+        args = [x, a64, b64]
+        got = f64(got)
+        for _ in range(12):
+            at = tuple(int(g.integers(n)) for n in args[base].shape)
+            up, down = [m.copy() for m in args], [m.copy() for m in args]
+            up[base][at] += h
+            down[base][at] -= h
+            diff = (loss(*up) - loss(*down)) / (2 * h)  # the loss is linear in each: exact up to fp64
+            assert abs(diff - got[at]) <= 2 * HALF * np.abs(got).max() + 1e-6, (name, at)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(3):
+        for t in (y, dx, da, db):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip((y, dx, da, db), eager))
+        c.check_forward(*c.forward())  # eager work of the program between the replays
 
 
 @pytest.mark.parametrize("T", [300, 2100])

@@ -236,3 +236,44 @@ def test_project_oracle_is_the_merged_weight():
             m += scaling[s] * b[s][:, :rank[s]] @ a[s][:rank[s]]
         np.testing.assert_allclose(y[t], m @ x[t], rtol=1e-12)
     assert (v[2:5] == 0).all() and (v[1, 2:] == 0).all()
+
+
+def _back(d, p, **kw):
+    v = dict(x=FAKE, c=None, e=None, w=FAKE, v=FAKE, dy=FAKE, dx=FAKE, da=FAKE, db=FAKE, ws=FAKE, ws_bytes=1 << 30)
+    v.update(kw)
+    return pkg.load().moe_lora_project_backward(
+        ctypes.byref(d), v["x"], v["c"], v["e"], v["w"], ctypes.byref(p) if p else None, v["v"], v["dy"], v["dx"], v["da"],
+        v["db"], v["ws"], v["ws_bytes"], None)
+
+
+def test_project_backward_refusals():
+    d = _lib.ProjDims(4, 64, 48, 64, 48)
+    bad = _lib.ERR_INVALID_ARGUMENT
+    for kw in (dict(dx=None, da=None, db=None), dict(x=None), dict(c=FAKE), dict(c=FAKE, e=FAKE),
+               dict(x=None, c=FAKE), dict(x=None, e=FAKE), dict(w=None), dict(v=None), dict(dy=None),
+               dict(ws=None), dict(dx=FAKE + 8), dict(da=FAKE + 2), dict(db=FAKE + 4), dict(x=FAKE + 8),
+               dict(dy=FAKE + 8), dict(v=FAKE + 4), dict(w=FAKE + 8)):
+        assert _back(d, _pool(), **kw) == bad, kw
+    assert _back(d, None) == bad
+    assert _back(d, _pool(), ws_bytes=64) == _lib.ERR_WORKSPACE_TOO_SMALL
+    assert _back(_lib.ProjDims(4, 64, 44, 64, 48), _pool()) == _lib.ERR_UNSUPPORTED
+
+
+def test_project_gradient_oracle_equals_differences():
+    g = np.random.Generator(np.random.PCG64(1))
+    T, K, N, S, R = 5, 4, 3, 2, 2
+    x, w, a, b, dy = (g.standard_normal(s) for s in ((T, K), (N, K), (S, R, K), (S, N, R), (T, N)))
+    slot, rank, scaling = np.array([0, 1, -1, 1, 0]), np.array([2, 1]), np.array([0.5, 2.0])
+    _, v = ref.project(x, w, slot, rank, scaling, a, b)
+    grads = ref.project_backward(dy, x, w, slot, rank, scaling, a, b, v)
+    args = [x, a, b]
+
+    def loss(x, a, b):
+        return (dy * ref.project(x, w, slot, rank, scaling, a, b)[0]).sum()
+
+    for i, got in enumerate(grads):
+        for at in np.ndindex(args[i].shape):
+            up, down = [m.copy() for m in args], [m.copy() for m in args]
+            up[i][at] += 1e-6
+            down[i][at] -= 1e-6
+            assert abs((loss(*up) - loss(*down)) / 2e-6 - got[at]) < 1e-7
