@@ -71,32 +71,37 @@ MOE_DEV int rank_of(const PoolView &P, int s) {
   return r < P.R ? r : P.R;
 }
 
-// Distinct adapters of a tile's rows: row slots into s_slot, the ascending list into s_list,
-// its length returned (uniform).  Called by the whole workgroup; s_bits: 16 words.
+// Distinct adapters of a tile's rows: row slots into s_slot (-1: none), the list of
+// slot | rank << 16 in ascending order into s_list, its length returned (uniform).  Called
+// by the whole workgroup; s_bits: 16 words.
 template <int ROWS, int NT>
 MOE_DEV int tile_adapters(const PoolView &P, int t0, int T, int *s_slot, int *s_list, uint32_t *s_bits) {
+  static_assert(ROWS <= NT, "one row per thread");
   const int tid = threadIdx.x;
   if (tid < 16) s_bits[tid] = 0u;
   __syncthreads();
-  for (int r = tid; r < ROWS; r += NT) {
-    int s = -1, rank;
-    if (P.S > 0 && t0 + r < T) s = adapter_of(P, t0 + r, rank);
-    s_slot[r] = s;
-    if (s >= 0) atomicOr(&s_bits[s >> 5], 1u << (s & 31));
+  int s = -1, rank = 0;
+  uint32_t before = 0;
+  if (tid < ROWS) {
+    if (P.S > 0 && t0 + tid < T) s = adapter_of(P, t0 + tid, rank);
+    s_slot[tid] = s;
+    if (s >= 0) before = atomicOr(&s_bits[s >> 5], 1u << (s & 31));
   }
   __syncthreads();
-  int n = 0;
+  int n = 0, at = 0;
 #pragma unroll
-  for (int w = 0; w < 16; ++w) n += __popc(s_bits[w]);
-  for (int s = tid; s < 512; s += NT) {
-    if ((s_bits[s >> 5] >> (s & 31)) & 1u) {
-      int at = __popc(s_bits[s >> 5] & ((1u << (s & 31)) - 1u));
-      for (int w = 0; w < (s >> 5); ++w) at += __popc(s_bits[w]);
-      s_list[at] = s;
-    }
+  for (int w = 0; w < 16; ++w) {
+    const int c = __popc(s_bits[w]);
+    at += w < (s >> 5) ? c : 0;
+    n += c;
   }
+  // the row that set its adapter's bit lists it
+  if (s >= 0 && !((before >> (s & 31)) & 1u))
+    s_list[at + __popc(s_bits[s >> 5] & ((1u << (s & 31)) - 1u))] = s | (rank << 16);
   __syncthreads();
   return __builtin_amdgcn_readfirstlane(n);
 }
+MOE_DEV int list_slot(int entry) { return entry & 0xffff; }
+MOE_DEV int list_rank(int entry) { return entry >> 16; }
 
 }  // namespace moe

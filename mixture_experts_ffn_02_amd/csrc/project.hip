@@ -22,20 +22,25 @@ namespace {
 
 // ------------------------------------------------------------------------ shrink
 // out[t, r] = sum_k x[t, k] m[slot][...] over a 16-token tile, for its j-th, (j + J)-th ...
-// distinct adapter.  TR = 0: m is A [S, R, K] (k contiguous, straight into the MFMA);
-// TR = 1: m is B [S, K, R] (r contiguous: a wavefront turns 32 x 16 pieces through LDS).
-// Stores s * out in bf16, and fp32 out (scaled if TR) where wanted, zeros past the rank.
+// distinct adapter.  TR = 0: m is A [S, R, K] (k contiguous); TR = 1: m is B [S, K, R] (r
+// contiguous: read back transposed from LDS).  Stores s * out in bf16, and fp32 out (scaled
+// if TR) where wanted, zeros past the rank.  Each wavefront takes a run of 64-wide K steps, G
+// of them in flight, loaded with neighbouring lanes on neighbouring bytes and turned into
+// MFMA operands through LDS of its own.
 constexpr int kShrinkWaves = 8;
 
 template <int RT, bool TR>
 __global__ __launch_bounds__(kShrinkWaves * 64) void shrink_kernel(const ShrinkArgs P) {
   constexpr int RP = RT * 16 + 1;
-  __shared__ float part[kShrinkWaves / 2][16 * RP];
-  __shared__ __attribute__((aligned(16))) uint16_t turn[TR ? kShrinkWaves * 32 * 16 * RT : 8];
+  constexpr int G = RT <= 2 ? 4 : 2, IT = 2 + 2 * RT;
+  constexpr int kStage = kShrinkWaves * (16 + RT * 16) * 64 * 2, kPart = kShrinkWaves * 16 * RP * 4;
+  __shared__ __attribute__((aligned(16))) unsigned char smem[kStage > kPart ? kStage : kPart];
+  __shared__ int s_slot[16];
+  float *part = reinterpret_cast<float *>(smem);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int t0 = blockIdx.x * 16;
   const int row = lane & 15, grp = lane >> 4;
-  int rank_row;
+  int rank_row = 0;
   const int t_row = t0 + row;
   int slot_row = t_row < P.T ? adapter_of(P.pool, t_row, rank_row) : -1;
   // rows whose adapter no earlier row of the tile has (bits of lanes 0..15)
@@ -46,225 +51,272 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void shrink_kernel(const ShrinkA
     if (i < row && o == slot_row) first = false;
   }
   uint32_t todo = (uint32_t)(__ballot(first) & 0xffffull);
+  if (tid < 16) s_slot[tid] = slot_row;
   const int R = P.pool.R;
+  __syncthreads();
   if (blockIdx.y == 0) {  // rows without an adapter
     for (int i = tid; i < 16 * R; i += kShrinkWaves * 64) {
       const int r = i / R, t = t0 + r;
-      int rk;
-      if (t < P.T && adapter_of(P.pool, t, rk) < 0) {
+      if (t < P.T && s_slot[r] < 0) {
         P.out_bf16[(size_t)t * R + i % R] = 0;
         if (P.out_f32) P.out_f32[(size_t)t * R + i % R] = 0.f;
       }
     }
   }
   for (int skip = 0; skip < (int)blockIdx.y && todo; ++skip) todo &= todo - 1;
-  const uint16_t *xr = P.x + (size_t)min(t_row, P.T - 1) * P.ldx;
+  uint16_t *stage = reinterpret_cast<uint16_t *>(smem) + wave * (16 + RT * 16) * 64;
+  uint16_t *stage_m = stage + 16 * 64;
+  const int lr = lane >> 3, lc = lane & 7;  // this lane's row of eight, and 16-byte chunk
+  const int st_off = lr * 64 + ((lc ^ lr) << 3);
+  const int steps = (P.K + 63) / 64, per = (steps + kShrinkWaves - 1) / kShrinkWaves;
+  const int s_begin = min(steps, wave * per), s_end = min(steps, s_begin + per);
+  const uint16_t *xr[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) xr[i] = P.x + (size_t)min(t0 + i * 8 + lr, P.T - 1) * P.ldx + lc * 8;
   while (todo) {
-    const int slot = __builtin_amdgcn_readlane(slot_row, __ffs(todo) - 1);
+    const int lead = __ffs(todo) - 1, slot = __builtin_amdgcn_readlane(slot_row, lead);
     for (int skip = 0; skip < (int)gridDim.y && todo; ++skip) todo &= todo - 1;
-    const int rank = rank_of(P.pool, slot);
+    const int rank = __builtin_amdgcn_readlane(rank_row, lead);
+    const float scale = P.pool.scaling[slot];
     for (int r0 = 0; r0 < rank; r0 += RT * 16) {
       f32x4_t acc[RT];
 #pragma unroll
       for (int i = 0; i < RT; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      const int steps = (P.K + 31) / 32;
-      const uint16_t *mp[RT];
+      // TR: a step's rows n, each 2 RT chunks of 8 ranks; else 16 RT rank rows of 8 chunks
+      const uint16_t *mp[2 * RT];
+      int m_n[2 * RT];
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        if constexpr (TR) {
-          mp[i] = P.m + (size_t)slot * P.K * R + min(r0 + i * 16 + (lane & 1) * 8, R - 8);
-        } else {
-          mp[i] = P.m + ((size_t)slot * R + min(r0 + i * 16 + row, R - 1)) * P.K;
-        }
+      for (int i = 0; i < 2 * RT; ++i) {
+        const int q = i * 64 + lane;
+        m_n[i] = q / (2 * RT);
+        if constexpr (TR)
+          mp[i] = P.m + ((size_t)slot * P.K + m_n[i]) * R + min(r0 + (q % (2 * RT)) * 8, R - 8);
+        else
+          mp[i] = P.m + ((size_t)slot * R + min(r0 + i * 8 + lr, R - 1)) * P.K + lc * 8;
       }
-      // G steps' loads in flight together; the last steps one by one, zeros past K
-      auto go = [&](int s, auto count, bool masked) {
-        constexpr int G = decltype(count)::value;
-        u32x4_t xf[G], mf[G][RT];
+      u32x4_t xg[G][2], mg[G][2 * RT];
+      auto load = [&](int g, int s) {  // zeros past the run or K
+        const bool in = s < s_end && s * 64 + lc * 8 < P.K;
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          const int k = (s + g * kShrinkWaves) * 32 + grp * 8;
-          const bool in = !masked || k < P.K;
-          xf[g] = in ? *reinterpret_cast<const u32x4_t *>(xr + k) : zero_u32x4();
+        for (int i = 0; i < 2; ++i) xg[g][i] = in ? *reinterpret_cast<const u32x4_t *>(xr[i] + s * 64) : zero_u32x4();
 #pragma unroll
-          for (int i = 0; i < RT; ++i) {
-            if constexpr (TR) {
-              const int n = (s + g * kShrinkWaves) * 32 + (lane >> 1);
-              mf[g][i] = !masked || n < P.K ? *reinterpret_cast<const u32x4_t *>(mp[i] + (size_t)n * R) : zero_u32x4();
-            } else {
-              mf[g][i] = in ? *reinterpret_cast<const u32x4_t *>(mp[i] + k) : zero_u32x4();
-            }
-          }
-        }
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-          if constexpr (TR) {
-            // [32][16] pieces of this wavefront, written and read back transposed (LDS
-            // operations of one wavefront complete in order)
-            uint16_t *tw = turn + wave * (32 * 16 * RT);
-#pragma unroll
-            for (int i = 0; i < RT; ++i)
-              *reinterpret_cast<u32x4_t *>(tw + i * 512 + (lane >> 1) * 16 + (lane & 1) * 8) = mf[g][i];
-            wave_lds_fence();
-#pragma unroll
-            for (int i = 0; i < RT; ++i) {
-              const uint16_t *p = tw + i * 512 + (grp * 8 + (row >> 2)) * 16 + 4 * (row & 3);
-              const u32x2_t lo = lds_read_tr(p), hi = lds_read_tr(p + 4 * 16);
-              mf[g][i] = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
-            }
-            wave_lds_fence();
-          }
-#pragma unroll
-          for (int i = 0; i < RT; ++i) acc[i] = mfma_16x16x32(xf[g], mf[g][i], acc[i]);
+        for (int i = 0; i < 2 * RT; ++i) {
+          if constexpr (TR)
+            mg[g][i] = s < s_end && s * 64 + m_n[i] < P.K
+                           ? *reinterpret_cast<const u32x4_t *>(mp[i] + (size_t)s * 64 * R)
+                           : zero_u32x4();
+          else
+            mg[g][i] = in ? *reinterpret_cast<const u32x4_t *>(mp[i] + s * 64) : zero_u32x4();
         }
       };
-      constexpr int G = RT <= 2 ? 4 : 2;
-      int s = wave;
-      for (; (s + (G - 1) * kShrinkWaves + 1) * 32 <= P.K; s += G * kShrinkWaves)
-        go(s, std::integral_constant<int, G>{}, false);
-      for (; s < steps; s += kShrinkWaves) go(s, std::integral_constant<int, 1>{}, true);
-      // join the wavefronts' sums, halving their number each time (a fixed order)
 #pragma unroll
-      for (int half = kShrinkWaves / 2; half >= 1; half >>= 1) {
-        __syncthreads();
-        if (wave >= half && wave < 2 * half)
+      for (int g = 0; g < G; ++g) load(g, s_begin + g);
+      __syncthreads();  // the last round's sums have been read
+      for (int s0 = s_begin; s0 < s_end; s0 += G) {
 #pragma unroll
-          for (int i = 0; i < RT; ++i)
+        for (int g = 0; g < G; ++g) {
+          if (s0 + g >= s_end) break;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) part[wave - half][(grp * 4 + q) * RP + i * 16 + row] = acc[i][q];
-        __syncthreads();
-        if (wave < half)
+          for (int i = 0; i < 2; ++i) *reinterpret_cast<u32x4_t *>(stage + i * 512 + st_off) = xg[g][i];
 #pragma unroll
-          for (int i = 0; i < RT; ++i)
+          for (int i = 0; i < 2 * RT; ++i)
+            *reinterpret_cast<u32x4_t *>(stage_m + i * 512 + (TR ? lane * 8 : st_off)) = mg[g][i];
+          if (s0 + g + G < s_end) load(g, s0 + g + G);
+          wave_lds_fence();
 #pragma unroll
-            for (int q = 0; q < 4; ++q) acc[i][q] += part[wave][(grp * 4 + q) * RP + i * 16 + row];
-      }
-      if (wave == 0) {
-        const float scale = P.pool.scaling[slot];
+          for (int kk = 0; kk < 2; ++kk) {
+            const int off = row * 64 + (((kk * 4 + grp) ^ (row & 7)) << 3);
+            const u32x4_t xf = *reinterpret_cast<const u32x4_t *>(stage + off);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int tr = grp * 4 + q, t = t0 + tr;
-          if (__shfl(slot_row, tr) != slot || t >= P.T) continue;
-#pragma unroll
-          for (int i = 0; i < RT; ++i) {
-            const int r = r0 + i * 16 + row;
-            if (r >= R) continue;
-            const float v = r < rank ? acc[i][q] : 0.f;
-            P.out_bf16[(size_t)t * R + r] = (uint16_t)f32_to_bf16(scale * v);
-            if (P.out_f32) P.out_f32[(size_t)t * R + r] = TR ? scale * v : v;
+            for (int i = 0; i < RT; ++i) {
+              u32x4_t mf;
+              if constexpr (TR) {
+                const uint16_t *p = stage_m + (kk * 32 + grp * 8 + (row >> 2)) * (16 * RT) + i * 16 + 4 * (row & 3);
+                const u32x2_t lo = lds_read_tr(p), hi = lds_read_tr(p + 4 * 16 * RT);
+                mf = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+              } else {
+                mf = *reinterpret_cast<const u32x4_t *>(stage_m + i * 16 * 64 + off);
+              }
+              acc[i] = mfma_16x16x32(xf, mf, acc[i]);
+            }
           }
+          wave_lds_fence();
         }
+      }
+      // join the wavefronts' sums (in their order)
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) part[(wave * 16 + grp * 4 + q) * RP + i * 16 + row] = acc[i][q];
+      __syncthreads();
+      for (int c = tid; c < 16 * RT * 16; c += kShrinkWaves * 64) {
+        const int tr = c / (RT * 16), rc = c % (RT * 16), t = t0 + tr, r = r0 + rc;
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kShrinkWaves; ++w) v += part[(w * 16 + tr) * RP + rc];
+        if (s_slot[tr] != slot || r >= R) continue;
+        if (r >= rank) v = 0.f;
+        P.out_bf16[(size_t)t * R + r] = (uint16_t)f32_to_bf16(scale * v);
+        if (P.out_f32) P.out_f32[(size_t)t * R + r] = TR ? scale * v : v;
       }
     }
     // ranks past the last chunk that the loop above wrote
-    if (wave == 0) {
-      const int done = (rank + RT * 16 - 1) / (RT * 16) * (RT * 16);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int tr = grp * 4 + q, t = t0 + tr;
-        if (__shfl(slot_row, tr) != slot || t >= P.T) continue;
-        for (int r = done + row; r < R; r += 16) {
-          P.out_bf16[(size_t)t * R + r] = 0;
-          if (P.out_f32) P.out_f32[(size_t)t * R + r] = 0.f;
-        }
+    const int done = (rank + RT * 16 - 1) / (RT * 16) * (RT * 16);
+    if (done < R) {
+      for (int c = tid; c < 16 * (R - done); c += kShrinkWaves * 64) {
+        const int tr = c / (R - done), t = t0 + tr, r = done + c % (R - done);
+        if (s_slot[tr] != slot) continue;
+        P.out_bf16[(size_t)t * R + r] = 0;
+        if (P.out_f32) P.out_f32[(size_t)t * R + r] = 0.f;
       }
     }
   }
 }
 
 // ------------------------------------------------------------------------ few tokens
-// y tile of 16 FM tokens x 16 FN columns; eight wavefronts split K (32-wide steps in turn)
-// and the tile's adapters, and join in LDS.
-constexpr int kFewWaves = 8;
-
-template <int FM, int FN>
-__global__ __launch_bounds__(kFewWaves * 64) void project_few_kernel(const ProjectArgs P) {
-  constexpr int BM = FM * 16, BN = FN * 16, NT = kFewWaves * 64;
+// y tile of 16 FM tokens x 16 FN columns; W wavefronts split K (a run of 64-wide steps each,
+// G of them in flight) and the tile's adapters, and join in LDS.  The first steps' loads are
+// out before the tile's adapters are listed, and the first adapters' before the steps'
+// products.  Eight neighbouring lanes load 128 contiguous bytes of a row, and each wavefront
+// turns its steps into MFMA operands through LDS of its own: loads in the operands' order
+// (neighbouring lanes in different rows) take one lane per cycle in the address path and
+// bounded the call (64 tokens, 2048 -> 4096: 13.6 us without adapters, 7.9 at 16 tokens).
+template <int FM, int FN, int W, int G>
+__global__ __launch_bounds__(W * 64) void project_few_kernel(const ProjectArgs P) {
+  constexpr int BM = FM * 16, BN = FN * 16, NT = W * 64;
   constexpr int PITCH = BN + 4;
-  __shared__ __attribute__((aligned(16))) float red[kFewWaves * BM * PITCH];
+  constexpr int ROWS = BM + BN, IT = ROWS / 8;  // x rows, then w rows
+  constexpr int kStage = W * ROWS * 64 * 2, kRed = W * BM * PITCH * 4;
+  __shared__ __attribute__((aligned(16))) unsigned char smem[kStage > kRed ? kStage : kRed];
   __shared__ int s_slot[BM], s_list[BM];
   __shared__ uint32_t s_bits[16];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int row = lane & 15, grp = lane >> 4;
   const int n0 = blockIdx.x * BN, t0 = blockIdx.y * BM;
   const PoolView &pool = P.pool;
   const int K = P.K, N = P.N;
-  const uint16_t *wp[FN], *xp[FM];
-#pragma unroll
-  for (int j = 0; j < FN; ++j) wp[j] = P.w + (size_t)min(n0 + j * 16 + row, N - 1) * K + grp * 8;
-#pragma unroll
-  for (int i = 0; i < FM; ++i) xp[i] = P.x + (size_t)min(t0 + i * 16 + row, P.T - 1) * P.ldx + grp * 8;
+  uint16_t *stage = reinterpret_cast<uint16_t *>(smem) + wave * ROWS * 64;
   f32x4_t acc[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  // G steps' loads in flight together; the last steps one by one, zeros past K
-  auto go = [&](int s, auto count, bool masked) {
-    constexpr int G = decltype(count)::value;
-    u32x4_t wf[G][FN], xf[G][FM];
+  const int steps = (K + 63) / 64, per = (steps + W - 1) / W;
+  const int s_begin = min(steps, wave * per), s_end = min(steps, s_begin + per);
+  const int lr = lane >> 3, lc = lane & 7;  // this lane's row of eight, and 16-byte chunk
+  const uint16_t *src[IT];
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const int k = (s + g * kFewWaves) * 32;
-      const bool in = !masked || k + grp * 8 < K;
+  for (int i = 0; i < IT; ++i) {
+    const int r = i * 8 + lr;
+    src[i] = r < BM ? P.x + (size_t)min(t0 + r, P.T - 1) * P.ldx : P.w + (size_t)min(n0 + r - BM, N - 1) * K;
+    src[i] += lc * 8;
+  }
+  const int st_off = lr * 64 + ((lc ^ lr) << 3);
+  u32x4_t rg[G][IT];
+  auto load = [&](int g, int s) {  // zeros past the run or K
+    const bool in = s < s_end && s * 64 + lc * 8 < K;
 #pragma unroll
-      for (int j = 0; j < FN; ++j) wf[g][j] = in ? *reinterpret_cast<const u32x4_t *>(wp[j] + k) : zero_u32x4();
-#pragma unroll
-      for (int i = 0; i < FM; ++i) xf[g][i] = in ? *reinterpret_cast<const u32x4_t *>(xp[i] + k) : zero_u32x4();
-    }
-#pragma unroll
-    for (int g = 0; g < G; ++g)
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = mfma_16x16x32(wf[g][j], xf[g][i], acc[i][j]);
+    for (int i = 0; i < IT; ++i) rg[g][i] = in ? *reinterpret_cast<const u32x4_t *>(src[i] + s * 64) : zero_u32x4();
   };
-  constexpr int G = 4;
-  int s = wave;
-  for (; (s + (G - 1) * kFewWaves + 1) * 32 <= K; s += G * kFewWaves) go(s, std::integral_constant<int, G>{}, false);
-  for (; s * 32 < K; s += kFewWaves) go(s, std::integral_constant<int, 1>{}, true);
-
-  const int n_list = tile_adapters<BM, NT>(pool, t0, P.T, s_slot, s_list, s_bits);
-  int slot_row[FM];
 #pragma unroll
-  for (int i = 0; i < FM; ++i) slot_row[i] = s_slot[i * 16 + row];
-  for (int q = wave; q < n_list; q += kFewWaves) {
-    const int slot = __builtin_amdgcn_readfirstlane(s_list[q]);
-    const int rank = rank_of(pool, slot);
-    for (int r0 = 0; r0 < rank; r0 += 32) {
-      const int r = r0 + grp * 8;
-      u32x4_t bf[FN], vf[FM];
+  for (int g = 0; g < G; ++g) load(g, s_begin + g);
+  const int n_list = tile_adapters<BM, NT>(pool, t0, P.T, s_slot, s_list, s_bits);
+
+  // the expand: 32 ranks of Q adapters' rows at a time
+  constexpr int Q = 2;
+  u32x4_t vf[FM], bf[Q][FN];
+  int slot[Q], rank[Q];
+  auto load_v = [&](int r0) {
+    const int r = r0 + grp * 8;
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+      vf[i] = r < pool.R ? *reinterpret_cast<const u32x4_t *>(
+                               P.ext_a + (size_t)min(t0 + i * 16 + row, P.T - 1) * pool.R + r)
+                         : zero_u32x4();
+  };
+  auto load_b = [&](int r0, int q0) {
+    const int r = r0 + grp * 8;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int at = q0 + q * W;
+      const int entry = at < n_list ? __builtin_amdgcn_readfirstlane(s_list[at]) : 0;
+      slot[q] = list_slot(entry);
+      rank[q] = list_rank(entry);
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
-        bf[j] = zero_u32x4();
         const int n = min(n0 + j * 16 + row, N - 1);
-        if (r < rank) bf[j] = *reinterpret_cast<const u32x4_t *>(P.ext_b + ((size_t)slot * N + n) * pool.R + r);
-        // ranks past the slot's inside its last 8 (whatever the pool holds there)
-        if (r < rank && r + 8 > rank)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (r + 2 * c >= rank) bf[j][c] = 0u;
-            else if (r + 2 * c + 1 >= rank) bf[j][c] &= 0xffffu;
-          }
+        bf[q][j] = r < rank[q] ? *reinterpret_cast<const u32x4_t *>(P.ext_b + ((size_t)slot[q] * N + n) * pool.R + r)
+                               : zero_u32x4();
       }
+    }
+  };
+  if (wave < n_list) {
+    load_v(0);
+    load_b(0, wave);
+  }
+  for (int s0 = s_begin; s0 < s_end; s0 += G) {
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        vf[i] = zero_u32x4();
-        if (r < rank && slot_row[i] == slot)
-          vf[i] = *reinterpret_cast<const u32x4_t *>(P.ext_a + (size_t)(t0 + i * 16 + row) * pool.R + r);
-      }
+    for (int g = 0; g < G; ++g) {
+      if (s0 + g >= s_end) break;
 #pragma unroll
-      for (int i = 0; i < FM; ++i)
+      for (int i = 0; i < IT; ++i) *reinterpret_cast<u32x4_t *>(stage + i * 512 + st_off) = rg[g][i];
+      if (s0 + g + G < s_end) load(g, s0 + g + G);
+      wave_lds_fence();
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          // (the column of a lane is one token: other requests' tokens take nothing, whatever
-          // this adapter holds)
-          const f32x4_t d = mfma_16x16x32(bf[j], vf[i], acc[i][j]);
-          if (slot_row[i] == slot) acc[i][j] = d;
+      for (int kk = 0; kk < 2; ++kk) {
+        const int off = row * 64 + (((kk * 4 + grp) ^ (row & 7)) << 3);
+        u32x4_t wf[FN];
+#pragma unroll
+        for (int j = 0; j < FN; ++j) wf[j] = *reinterpret_cast<const u32x4_t *>(stage + (BM + j * 16) * 64 + off);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+          const u32x4_t xf = *reinterpret_cast<const u32x4_t *>(stage + i * 16 * 64 + off);
+#pragma unroll
+          for (int j = 0; j < FN; ++j) acc[i][j] = mfma_16x16x32(wf[j], xf, acc[i][j]);
         }
+      }
+      wave_lds_fence();
     }
   }
+  if (wave < n_list) {
+    int slot_row[FM];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) slot_row[i] = s_slot[i * 16 + row];
+    for (int r0 = 0; r0 < pool.R; r0 += 32) {
+      const int r = r0 + grp * 8;
+      if (r0 > 0) load_v(r0);
+      for (int q0 = wave; q0 < n_list; q0 += Q * W) {
+        if (r0 > 0 || q0 > wave) load_b(r0, q0);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          if (r0 >= rank[q]) continue;
+          // ranks past the adapter's inside its last 8: zeros, whatever the pool holds there
+          if ((rank[q] & 7) != 0 && r < rank[q] && r + 8 > rank[q])
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                if (r + 2 * c >= rank[q]) bf[q][j][c] = 0u;
+                else if (r + 2 * c + 1 >= rank[q]) bf[q][j][c] &= 0xffffu;
+              }
+          // a lane's column is one token: those of other requests take nothing from this
+          // adapter, whatever it holds
+#pragma unroll
+          for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+              const f32x4_t d = mfma_16x16x32(bf[q][j], vf[i], acc[i][j]);
+              if (slot_row[i] == slot[q]) acc[i][j] = d;
+            }
+        }
+      }
+    }
+  }
+  float *red = reinterpret_cast<float *>(smem);
+  __syncthreads();  // the stages are free
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -275,7 +327,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void project_few_kernel(const Proje
     const int t = c / (BN / 4), n = (c % (BN / 4)) * 4;
     f32x4_t v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int w = 0; w < kFewWaves; ++w) v += *reinterpret_cast<const f32x4_t *>(&red[(w * BM + t) * PITCH + n]);
+    for (int w = 0; w < W; ++w) v += *reinterpret_cast<const f32x4_t *>(&red[(w * BM + t) * PITCH + n]);
     if (t0 + t < P.T && n0 + n < N)
       *reinterpret_cast<u32x2_t *>(P.y + (size_t)(t0 + t) * P.ldy + n0 + n) =
           u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
@@ -434,9 +486,10 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void project_tile_kernel(const Proj
   const int chunks = (pool.R + 63) / 64;  // 64-rank chunks per adapter
   const int exts = n_list * chunks;
   auto ext_of = [&](int e, int &slot, int &r0, int &rank) {
-    slot = __builtin_amdgcn_readfirstlane(s_list[e / chunks]);
+    const int entry = __builtin_amdgcn_readfirstlane(s_list[e / chunks]);
+    slot = list_slot(entry);
     r0 = (e % chunks) * 64;
-    rank = rank_of(pool, slot);
+    rank = list_rank(entry);
   };
   auto main_step = [&](int buf, int s) {
     dma_wait_all();
@@ -535,17 +588,17 @@ int launch_shrink(const ShrinkArgs &a, hipStream_t s) {
   return ok();
 }
 
-template <int FN>
-int launch_few(const ProjectArgs &a, hipStream_t s) {
-  const int fm = a.T <= 16 ? 1 : a.T <= 32 ? 2 : 4;
-  const dim3 grid((a.N + FN * 16 - 1) / (FN * 16), (a.T + fm * 16 - 1) / (fm * 16));
-  if (fm == 1)
-    project_few_kernel<1, FN><<<grid, kFewWaves * 64, 0, s>>>(a);
-  else if (fm == 2)
-    project_few_kernel<2, FN><<<grid, kFewWaves * 64, 0, s>>>(a);
-  else
-    project_few_kernel<4, FN><<<grid, kFewWaves * 64, 0, s>>>(a);
+template <int FM, int FN, int W, int G>
+int launch_few_tile(const ProjectArgs &a, hipStream_t s) {
+  const dim3 grid((a.N + FN * 16 - 1) / (FN * 16), (a.T + FM * 16 - 1) / (FM * 16));
+  project_few_kernel<FM, FN, W, G><<<grid, W * 64, 0, s>>>(a);
   return ok();
+}
+
+int launch_few(const ProjectArgs &a, hipStream_t s) {
+  if (a.T <= 16) return launch_few_tile<1, 1, 8, 4>(a, s);
+  if (a.T <= 32) return launch_few_tile<2, 1, 8, 4>(a, s);
+  return launch_few_tile<4, 1, 8, 4>(a, s);
 }
 
 template <int BM, int BN, int WM, int WN, bool NN>
@@ -576,8 +629,7 @@ int launch_project(const ProjectArgs &a, float *v, hipStream_t s) {
     const int st = launch_shrink<false>(sh, s);
     if (st != ST_OK) return st;
   }
-  if (a.T <= kFewTokens)
-    return (a.N + 31) / 32 >= 96 ? launch_few<2>(a, s) : launch_few<1>(a, s);
+  if (a.T <= kFewTokens) return launch_few(a, s);
   return launch_product<false>(a, s);
 }
 
