@@ -4,6 +4,9 @@
 #include "common.h"
 #include "kernels.h"
 
+// (a lambda of a kernel left out of line would take its captures through memory)
+#define MOE_INLINE __attribute__((always_inline))
+
 namespace moe {
 
 // 16 zero bytes for lanes whose chunk lies outside its matrix (a masked lane still reads)
@@ -20,12 +23,15 @@ MOE_DEV void dma16(const void *src, uint32_t lds) {
       "global_load_lds_dwordx4 %1, off\n\t"
       "s_mov_b32 m0, %0"
       : "=&s"(saved)
-      : "v"(src), "s"(lds)
+      : "v"(src), "s"(__builtin_amdgcn_readfirstlane((int)lds))
       : "memory");
 }
 // the same with a wave-uniform base and a 32-bit byte offset per lane
 MOE_DEV void dma16(const void *base, uint32_t off, uint32_t lds) {
   uint32_t saved;
+  const uint64_t b = reinterpret_cast<uint64_t>(base);
+  const uint64_t sb = ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(b >> 32)) << 32) |
+                      (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)b);
   asm volatile(
       "s_mov_b32 %0, m0\n\t"
       "s_mov_b32 m0, %3\n\t"
@@ -33,7 +39,7 @@ MOE_DEV void dma16(const void *base, uint32_t off, uint32_t lds) {
       "global_load_lds_dwordx4 %1, %2\n\t"
       "s_mov_b32 m0, %0"
       : "=&s"(saved)
-      : "v"(off), "s"(base), "s"(lds)
+      : "v"(off), "s"(sb), "s"(__builtin_amdgcn_readfirstlane((int)lds))
       : "memory");
 }
 MOE_DEV void dma_wait_all() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
@@ -71,19 +77,17 @@ MOE_DEV int rank_of(const PoolView &P, int s) {
   return r < P.R ? r : P.R;
 }
 
-// Distinct adapters of a tile's rows: row slots into s_slot (-1: none), the list of
-// slot | rank << 16 in ascending order into s_list, its length returned (uniform).  Called
-// by the whole workgroup; s_bits: 16 words.
+// Distinct adapters of a tile's rows, thread r giving row r's (slot -1: none): row slots into
+// s_slot, the list of slot | rank << 16 in ascending order into s_list, its length returned
+// (uniform).  Called by the whole workgroup; s_bits: 16 words.
 template <int ROWS, int NT>
-MOE_DEV int tile_adapters(const PoolView &P, int t0, int T, int *s_slot, int *s_list, uint32_t *s_bits) {
+MOE_DEV int list_adapters(int s, int rank, int *s_slot, int *s_list, uint32_t *s_bits) {
   static_assert(ROWS <= NT, "one row per thread");
   const int tid = threadIdx.x;
   if (tid < 16) s_bits[tid] = 0u;
   __syncthreads();
-  int s = -1, rank = 0;
   uint32_t before = 0;
   if (tid < ROWS) {
-    if (P.S > 0 && t0 + tid < T) s = adapter_of(P, t0 + tid, rank);
     s_slot[tid] = s;
     if (s >= 0) before = atomicOr(&s_bits[s >> 5], 1u << (s & 31));
   }
@@ -100,6 +104,13 @@ MOE_DEV int tile_adapters(const PoolView &P, int t0, int T, int *s_slot, int *s_
     s_list[at + __popc(s_bits[s >> 5] & ((1u << (s & 31)) - 1u))] = s | (rank << 16);
   __syncthreads();
   return __builtin_amdgcn_readfirstlane(n);
+}
+template <int ROWS, int NT>
+MOE_DEV int tile_adapters(const PoolView &P, int t0, int T, int *s_slot, int *s_list, uint32_t *s_bits) {
+  const int tid = threadIdx.x;
+  int s = -1, rank = 0;
+  if (tid < ROWS && P.S > 0 && t0 + tid < T) s = adapter_of(P, t0 + tid, rank);
+  return list_adapters<ROWS, NT>(s, rank, s_slot, s_list, s_bits);
 }
 MOE_DEV int list_slot(int entry) { return entry & 0xffff; }
 MOE_DEV int list_rank(int entry) { return entry >> 16; }

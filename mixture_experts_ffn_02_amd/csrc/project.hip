@@ -29,10 +29,10 @@ namespace {
 // MFMA operands through LDS of its own.
 constexpr int kShrinkWaves = 8;
 
-template <int RT, bool TR>
-__global__ __launch_bounds__(kShrinkWaves * 64) void shrink_kernel(const ShrinkArgs P) {
+template <int RT, bool TR, bool LONG>
+__global__ __launch_bounds__(kShrinkWaves * 64, LONG ? 3 : 2) void shrink_kernel(const ShrinkArgs P) {
   constexpr int RP = RT * 16 + 1;
-  constexpr int G = RT <= 2 ? 4 : 2, IT = 2 + 2 * RT;
+  constexpr int G = LONG ? (RT <= 2 ? 2 : 1) : RT <= 2 ? 4 : 2;
   constexpr int kStage = kShrinkWaves * (16 + RT * 16) * 64 * 2, kPart = kShrinkWaves * 16 * RP * 4;
   __shared__ __attribute__((aligned(16))) unsigned char smem[kStage > kPart ? kStage : kPart];
   __shared__ int s_slot[16];
@@ -335,6 +335,22 @@ __global__ __launch_bounds__(W * 64) void project_few_kernel(const ProjectArgs P
 }
 
 // ------------------------------------------------------------------------ many tokens
+// 8 outputs of a token whose adapter may hold what is not finite: NaN where a row (column,
+// NN) of the adapter's expand does.  Rare: the tile found such a value.
+template <bool NN>
+MOE_DEV void restore_odd(const ProjectArgs &P, int slot, int n, u32x4_t &v) {
+  if (slot < 0) return;
+  const int rank = rank_of(P.pool, slot), R = P.pool.R;
+  for (int i = 0; i < 8; ++i) {
+    bool odd = false;
+    for (int r = 0; r < rank; ++r) {
+      const uint16_t b = NN ? P.ext_b[((size_t)slot * R + r) * P.N + n + i] : P.ext_b[((size_t)slot * P.N + n + i) * R + r];
+      odd |= (b & 0x7f80u) == 0x7f80u;
+    }
+    if (odd) v[i >> 1] = (v[i >> 1] & (i & 1 ? 0x0000ffffu : 0xffff0000u)) | (0x7fc0u << (16 * (i & 1)));
+  }
+}
+
 // One BM x BN tile per workgroup, 64-wide K steps double-buffered in LDS, both operands by
 // DMA loads one step ahead (rows of x and W past the matrix repeat its last row, chunks
 // past K read zeros).  The expand's steps follow in the same pipeline.
@@ -345,14 +361,15 @@ __global__ __launch_bounds__(W * 64) void project_few_kernel(const ProjectArgs P
 // bits that the lanes of a transposed read differ in.  The DMA writes LDS in lane order, so
 // the swizzle picks the source chunk of each lane.
 template <int BM, int BN, int WM, int WN, bool NN>
-__global__ __launch_bounds__(WM *WN * 64, 2) void project_tile_kernel(const ProjectArgs P) {
+__global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) void project_tile_kernel(const ProjectArgs P) {
   constexpr int NT = WM * WN * 64;
   constexpr int WTM = BM / WM, WTN = BN / WN, FM = WTM / 16, FN = WTN / 16;
   constexpr int A_IT = BM * 8 / NT, B_IT = BN * 8 / NT;
   constexpr int BCH = BN / 8;  // chunks per row of B (NN)
   constexpr int SWZ = BN / 16 < 8 ? BN / 16 - 1 : 7;  // its pairs' swizzle stays inside a row
-  __shared__ __attribute__((aligned(16))) uint16_t As[2][BM * 64];
-  __shared__ __attribute__((aligned(16))) uint16_t Bs[2][BN * 64];
+  __shared__ __attribute__((aligned(16))) uint16_t smem[2 * (BM + BN) * 64];
+  uint16_t(*As)[BM * 64] = reinterpret_cast<uint16_t(*)[BM * 64]>(smem);
+  uint16_t(*Bs)[BN * 64] = reinterpret_cast<uint16_t(*)[BN * 64]>(smem + 2 * BM * 64);
   __shared__ int s_slot[BM], s_list[BM];
   __shared__ uint32_t s_bits[16];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -400,7 +417,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void project_tile_kernel(const Proj
   const uint32_t a_lds[2] = {lds_byte(&As[0][0]) + wave * 1024, lds_byte(&As[1][0]) + wave * 1024};
   const uint32_t b_lds[2] = {lds_byte(&Bs[0][0]) + wave * 1024, lds_byte(&Bs[1][0]) + wave * 1024};
 
-  auto issue_full = [&](int buf, int k0) {
+  auto issue_full = [&](int buf, int k0) MOE_INLINE {
     const uint16_t *ab = a_base + k0;
     const uint16_t *bb = NN ? b_base + (size_t)k0 * N : b_base + k0;
 #pragma unroll
@@ -408,7 +425,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void project_tile_kernel(const Proj
 #pragma unroll
     for (int i = 0; i < B_IT; ++i) dma16(bb, b_off[i], b_lds[buf] + i * NT * 16);
   };
-  auto issue_tail = [&](int buf, int k0) {  // chunks past K are zeros
+  auto issue_tail = [&](int buf, int k0) MOE_INLINE {  // chunks past K are zeros
     const char *ab = reinterpret_cast<const char *>(a_base + k0);
     const char *bb = reinterpret_cast<const char *>(NN ? b_base + (size_t)k0 * N : b_base + k0);
 #pragma unroll
@@ -419,7 +436,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void project_tile_kernel(const Proj
       dma16(k0 + b_k[i] < K ? bb + b_off[i] : reinterpret_cast<const char *>(kZeroChunk), b_lds[buf] + i * NT * 16);
   };
   // ranks [r0, r0 + 64) of one adapter
-  auto issue_ext = [&](int buf, int slot, int r0, int rank) {
+  auto issue_ext = [&](int buf, int slot, int r0, int rank) MOE_INLINE {
     const char *z = reinterpret_cast<const char *>(kZeroChunk);
 #pragma unroll
     for (int i = 0; i < A_IT; ++i) {
@@ -460,112 +477,160 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void project_tile_kernel(const Proj
   // (row / 4) | 4 (grp & 1); columns 4 (row % 4) of a 16-wide piece (one 32-byte pair)
   const int tr_row = grp * 8 + (row >> 2), tr_swz = ((row >> 2) | ((grp & 1) << 2)) & SWZ;
 
-  auto fragments = [&](int buf, int kk, u32x4_t(&af)[FM], u32x4_t(&bf)[FN]) {
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-      af[i] = *reinterpret_cast<const u32x4_t *>(&As[buf][(wm * WTM + i * 16) * 64 + a_frag[kk]]);
-#pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      if constexpr (!NN) {
-        bf[j] = *reinterpret_cast<const u32x4_t *>(&Bs[buf][(wn * WTN + j * 16) * 64 + b_frag[kk]]);
-      } else {
-        const int pair = (wn * WTN) / 16 + j;
-        const uint16_t *p = &Bs[buf][(kk * 32 + tr_row) * BN + ((pair ^ tr_swz) << 4) + 4 * (row & 3)];
-        const u32x2_t lo = lds_read_tr(p), hi = lds_read_tr(p + 4 * BN);
-        bf[j] = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
-      }
+  // the c-th of the reads that bring one 32-wide half's operands into registers
+  constexpr int kReads = FM + (NN ? 2 * FN : FN);
+  auto read = [&](int buf, int kk, int c, u32x4_t(&af)[FM], u32x4_t(&bf)[FN]) MOE_INLINE {
+    if (c < FM) {
+      af[c] = *reinterpret_cast<const u32x4_t *>(&As[buf][(wm * WTM + c * 16) * 64 + a_frag[kk]]);
+    } else if constexpr (!NN) {
+      bf[c - FM] = *reinterpret_cast<const u32x4_t *>(&Bs[buf][(wn * WTN + (c - FM) * 16) * 64 + b_frag[kk]]);
+    } else {
+      const int j = (c - FM) >> 1, h = (c - FM) & 1;
+      const int pair = (wn * WTN) / 16 + j;
+      const u32x2_t v = lds_read_tr(
+          &Bs[buf][(kk * 32 + tr_row + 4 * h) * BN + ((pair ^ tr_swz) << 4) + 4 * (row & 3)]);
+      bf[j][2 * h] = v[0];
+      bf[j][2 * h + 1] = v[1];
     }
   };
 
-  const int steps = (K + 63) / 64;
-  if (steps == 1 && K < 64)
-    issue_tail(0, 0);
-  else
-    issue_full(0, 0);
-  const int n_list = tile_adapters<BM, NT>(pool, t0, P.T, s_slot, s_list, s_bits);
+  // Pipeline of a step: its first half's operands are in registers when it begins; the
+  // second half's are read among the first half's products, then the next step's data must
+  // have landed (one barrier: also every wavefront has left this buffer), and the DMA of the
+  // step after it goes out into this buffer, among the second half's products, with the
+  // reads of the next step's first operands.
+  const int steps = (K + 63) / 64, full = K / 64;
   const int chunks = (pool.R + 63) / 64;  // 64-rank chunks per adapter
-  const int exts = n_list * chunks;
-  auto ext_of = [&](int e, int &slot, int &r0, int &rank) {
+  int exts = 0;                           // known once the adapters are listed
+  auto ext_of = [&](int e, int &slot, int &r0, int &rank) MOE_INLINE {
     const int entry = __builtin_amdgcn_readfirstlane(s_list[e / chunks]);
     slot = list_slot(entry);
     r0 = (e % chunks) * 64;
     rank = list_rank(entry);
   };
-  auto main_step = [&](int buf, int s) {
-    dma_wait_all();
-    __syncthreads();  // step s has landed, and every wavefront has left step s - 1
-    if ((s + 2) * 64 <= K) {
-      issue_full(buf ^ 1, (s + 1) * 64);
-    } else if (s + 1 < steps) {
-      issue_tail(buf ^ 1, (s + 1) * 64);
-    } else if (exts > 0) {
+  auto issue = [&](int buf, int s) MOE_INLINE {
+    if (s < full) {
+      issue_full(buf, s * 64);
+    } else if (s < steps) {
+      issue_tail(buf, s * 64);
+    } else if (s < steps + exts) {
       int slot, r0, rank;
-      ext_of(0, slot, r0, rank);
-      issue_ext(buf ^ 1, slot, r0, rank);
-    }
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      u32x4_t af[FM], bf[FN];
-      fragments(buf, kk, af, bf);
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = mfma_16x16x32(bf[j], af[i], acc[i][j]);
-      __builtin_amdgcn_sched_barrier(0);
+      ext_of(s - steps, slot, r0, rank);
+      issue_ext(buf, slot, r0, rank);
     }
   };
+  issue(0, 0);
+  exts = chunks * tile_adapters<BM, NT>(pool, t0, P.T, s_slot, s_list, s_bits);
+  dma_wait_all();
+  __syncthreads();
+  issue(1, 1);
+  u32x4_t af0[FM], bf0[FN], af1[FM], bf1[FN];
+#pragma unroll
+  for (int c = 0; c < kReads; ++c) read(0, 0, c, af0, bf0);
+
+  // products of one half among the reads of (buf, kk)
+  auto half = [&](u32x4_t(&af)[FM], u32x4_t(&bf)[FN], int buf, int kk, u32x4_t(&an)[FM], u32x4_t(&bn)[FN]) MOE_INLINE {
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int c = 0; c < kReads; ++c) read(buf, kk, c, an, bn);
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] = mfma_16x16x32(bf[j], af[i], acc[i][j]);
+#pragma unroll
+    for (int c = 0; c < kReads; ++c) {  // an LDS read, then a share of the products
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, FM * FN / kReads, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // (two steps to an iteration and the branches of issue() between the halves: with both
+  // halves in one basic block, or one step to an iteration, the register allocator moved
+  // accumulators about on every step)
+  auto main_step = [&](int buf, int s) MOE_INLINE {
+    half(af0, bf0, buf, 1, af1, bf1);
+    dma_wait_all();
+    __syncthreads();
+    issue(buf, s + 2);
+    half(af1, bf1, buf ^ 1, 0, af0, bf0);  // (past the last step the reads bring what nothing uses)
+  };
+#pragma unroll 1
   for (int s = 0; s < steps; s += 2) {
     main_step(0, s);
     if (s + 1 < steps) main_step(1, s + 1);
   }
+
+  // The expand.  Other requests' rows of the A operand are zeros; so that nothing that an
+  // adapter holds reaches them as 0 * inf or 0 * NaN, what is not finite in its rows is taken
+  // out here and marks the adapter, whose outputs get it back at the end.  (Selecting
+  // accumulators by row instead kept them out of the accumulation registers.)
+  if (tid == 0) s_bits[0] = 0u;
+#pragma unroll 1
   for (int e = 0; e < exts; ++e) {
     const int buf = (steps + e) & 1;
     int slot, r0, rank;
     ext_of(e, slot, r0, rank);
     const int left = rank - r0;
-    dma_wait_all();
-    __syncthreads();
-    if (e + 1 < exts) {
-      int slot2, r02, rank2;
-      ext_of(e + 1, slot2, r02, rank2);
-      issue_ext(buf ^ 1, slot2, r02, rank2);
-    }
-    if (!NN && left > 0 && left < 64 && (left & 7) != 0) {
-      // ranks past the slot's inside its last 8: zeros, whatever the pool holds there
-      for (int n = tid; n < BN; n += NT) {
-        uint16_t *p = &Bs[buf][n * 64 + (((left >> 3) ^ (n & 7)) << 3)];
-        for (int c = left & 7; c < 8; ++c) p[c] = 0;
+    if (left > 0) {
+      bool odd = false;
+#pragma unroll
+      for (int i = 0; i < B_IT; ++i) {
+        u32x4_t *p = reinterpret_cast<u32x4_t *>(&Bs[buf][(i * NT + tid) * 8]);
+        u32x4_t v = *p;
+        bool change = false;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint32_t half_mask = c & 1 ? 0xffff0000u : 0x0000ffffu;
+          // (NN = 0: ranks past the adapter's, whatever the pool holds there)
+          const bool past = !NN && b_k[i] + c >= left;
+          const bool bad = (v[c >> 1] & half_mask & 0x7f807f80u) == (half_mask & 0x7f807f80u);
+          odd |= bad && !past;
+          change |= bad || past;
+          v[c >> 1] &= bad || past ? ~half_mask : 0xffffffffu;
+        }
+        if (change) *p = v;
       }
+      if (odd) atomicOr(&s_bits[0], 1u);
       __syncthreads();
     }
+#pragma unroll 1
     for (int kk = 0; kk < 2 && kk * 32 < left; ++kk) {
-      u32x4_t af[FM], bf[FN];
-      fragments(buf, kk, af, bf);
-      // a lane's column is one token: those of other requests take nothing from this
-      // adapter, whatever it holds
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const bool mine = s_slot[wm * WTM + i * 16 + row] == slot;
+      for (int c = 0; c < kReads; ++c) read(buf, kk, c, af1, bf1);
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          const f32x4_t d = mfma_16x16x32(bf[j], af[i], acc[i][j]);
+      for (int i = 0; i < FM; ++i)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) acc[i][j][q] = mine ? d[q] : acc[i][j][q];
-        }
-        __builtin_amdgcn_sched_barrier(0);  // (a row of tiles at a time: few temporaries)
-      }
+        for (int j = 0; j < FN; ++j) acc[i][j] = mfma_16x16x32(bf1[j], af1[i], acc[i][j]);
+    }
+    if (e + 1 < exts) {
+      dma_wait_all();
+      __syncthreads();
+      if (e + 2 < exts) issue(buf, steps + e + 2);
     }
   }
+  // The tile leaves through LDS (rows of BN bf16, 16-byte chunks XOR-swizzled by the row), so
+  // that neighbouring lanes store neighbouring bytes.
+  constexpr int OCH = BN / 8, OSW = OCH < 16 ? OCH - 1 : 15;
+  __syncthreads();
+  const bool odd_adapter = s_bits[0] != 0u;
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
-    const int t = t0 + wm * WTM + i * 16 + row;
-    if (t >= P.T) continue;
+    const int r = wm * WTM + i * 16 + row;
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
-      const int n = n0 + wn * WTN + j * 16 + grp * 4;
-      if (n < N)
-        *reinterpret_cast<u32x2_t *>(P.y + (size_t)t * P.ldy + n) =
-            u32x2_t{pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3])};
+      const int c = (wn * WTN + j * 16) / 8 + (grp >> 1);
+      *reinterpret_cast<u32x2_t *>(&smem[r * BN + ((c ^ (r & OSW)) << 3) + (grp & 1) * 4]) =
+          u32x2_t{pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3])};
+    }
+  }
+  __syncthreads();
+#pragma unroll 4
+  for (int q = tid; q < BM * OCH; q += NT) {
+    const int r = q / OCH, c = q % OCH, t = t0 + r, n = n0 + c * 8;
+    if (t < P.T && n < N) {
+      u32x4_t v = *reinterpret_cast<const u32x4_t *>(&smem[r * BN + ((c ^ (r & OSW)) << 3)]);
+      if (odd_adapter) restore_odd<NN>(P, s_slot[r], n, v);
+      *reinterpret_cast<u32x4_t *>(P.y + (size_t)t * P.ldy + n) = v;
     }
   }
 }
@@ -574,18 +639,24 @@ int ok() { return hipGetLastError() == hipSuccess ? ST_OK : ST_HIP; }
 
 constexpr int kFewTokens = 256;
 
+template <bool TR, bool LONG>
+int launch_shrink_ranks(const ShrinkArgs &a, hipStream_t s) {
+  const dim3 grid((a.T + 15) / 16, LONG ? 1 : 16);
+  if (a.pool.R <= 16)
+    shrink_kernel<1, TR, LONG><<<grid, kShrinkWaves * 64, 0, s>>>(a);
+  else if (a.pool.R <= 32)
+    shrink_kernel<2, TR, LONG><<<grid, kShrinkWaves * 64, 0, s>>>(a);
+  else
+    shrink_kernel<4, TR, LONG><<<grid, kShrinkWaves * 64, 0, s>>>(a);
+  return ok();
+}
+
+// A decode-sized batch takes a workgroup per (tile, adapter): up to 16 adapters meet in a
+// tile of 16 requests.  In longer batches a tile's few adapters follow each other, and two
+// workgroups share a compute unit.
 template <bool TR>
 int launch_shrink(const ShrinkArgs &a, hipStream_t s) {
-  // a decode-sized batch takes a workgroup per (tile, adapter): up to 16 adapters meet in a
-  // tile of 16 requests; in longer batches a tile's few adapters follow each other
-  const dim3 grid((a.T + 15) / 16, a.T <= 1024 ? 16 : 1);
-  if (a.pool.R <= 16)
-    shrink_kernel<1, TR><<<grid, kShrinkWaves * 64, 0, s>>>(a);
-  else if (a.pool.R <= 32)
-    shrink_kernel<2, TR><<<grid, kShrinkWaves * 64, 0, s>>>(a);
-  else
-    shrink_kernel<4, TR><<<grid, kShrinkWaves * 64, 0, s>>>(a);
-  return ok();
+  return a.T <= 1024 ? launch_shrink_ranks<TR, false>(a, s) : launch_shrink_ranks<TR, true>(a, s);
 }
 
 template <int FM, int FN, int W, int G>
@@ -611,7 +682,7 @@ int launch_tiles(const ProjectArgs &a, hipStream_t s) {
 template <bool NN>
 int launch_product(const ProjectArgs &a, hipStream_t s) {
   auto tiles = [&](int b) { return (long long)((a.T + b - 1) / b) * ((a.N + b - 1) / b); };
-  if (tiles(256) >= 192) return launch_tiles<256, 256, 2, 4, NN>(a, s);
+  if (tiles(256) >= 192) return launch_tiles<256, 256, 2, 2, NN>(a, s);
   if (tiles(128) >= 160) return launch_tiles<128, 128, 2, 2, NN>(a, s);
   return launch_tiles<64, 64, 2, 2, NN>(a, s);
 }

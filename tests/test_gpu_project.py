@@ -289,6 +289,30 @@ def test_requests_do_not_reach_each_other(T, mixed):
     assert torch.isnan(y2[victim]).all()
 
 
+@pytest.mark.parametrize("T", [40, 600, 3000])
+def test_an_adapter_that_is_not_finite_shows_in_its_own_rows(T):
+    """Infinities and NaN in two rows of one adapter's B: its tokens get NaN or infinities in those two
+    outputs and their values elsewhere; nobody else's change."""
+    c = Case(T, 128, 1032, 3, 24, mixed=False, dirty=False)
+    c.slot[:] = runs(c.g, T, 3, 7)
+    c.slot[T // 2:T // 2 + 5] = 1
+    c.pool.token_slot.copy_(torch.from_numpy(c.slot))
+    y, _ = c.forward()
+    y = y.clone()
+    r = int(c.rank[1]) if c.rank[1] > 0 else 0
+    if r == 0:
+        c.pool.rank[1] = c.rank[1] = r = 13
+        y = c.forward()[0].clone()
+    c.b[1, 5, r - 1], c.b[1, 700, 0] = float("nan"), float("inf")
+    y2 = c.forward()[0]
+    mine = torch.from_numpy(c.slot == 1).to(dev())
+    assert torch.equal(y[~mine], y2[~mine])
+    odd = torch.zeros(1032, dtype=torch.bool, device=dev())
+    odd[[5, 700]] = True
+    assert not torch.isfinite(y2[mine][:, odd]).any()
+    assert torch.equal(y[mine][:, ~odd], y2[mine][:, ~odd])
+
+
 def test_same_result_from_every_call_and_stream():
     c = Case(500, 512, 776, 6, 32)
     y, v = c.forward()
