@@ -1,6 +1,8 @@
 // Shared pieces of the pooled-adapter projection kernels (gfx950).
 #pragma once
 
+#include <type_traits>
+
 #include "common.h"
 #include "kernels.h"
 
@@ -23,15 +25,12 @@ MOE_DEV void dma16(const void *src, uint32_t lds) {
       "global_load_lds_dwordx4 %1, off\n\t"
       "s_mov_b32 m0, %0"
       : "=&s"(saved)
-      : "v"(src), "s"(__builtin_amdgcn_readfirstlane((int)lds))
+      : "v"(src), "s"(lds)
       : "memory");
 }
 // the same with a wave-uniform base and a 32-bit byte offset per lane
 MOE_DEV void dma16(const void *base, uint32_t off, uint32_t lds) {
   uint32_t saved;
-  const uint64_t b = reinterpret_cast<uint64_t>(base);
-  const uint64_t sb = ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(b >> 32)) << 32) |
-                      (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)b);
   asm volatile(
       "s_mov_b32 %0, m0\n\t"
       "s_mov_b32 m0, %3\n\t"
@@ -39,10 +38,34 @@ MOE_DEV void dma16(const void *base, uint32_t off, uint32_t lds) {
       "global_load_lds_dwordx4 %1, %2\n\t"
       "s_mov_b32 m0, %0"
       : "=&s"(saved)
-      : "v"(off), "s"(sb), "s"(__builtin_amdgcn_readfirstlane((int)lds))
+      : "v"(off), "s"(base), "s"(lds)
       : "memory");
 }
+// The same, to lds + LDS, where on is not 0 and nothing where it is (wave-uniform), without a
+// branch.  For code that all 64 lanes run: the mask is set back to all of them.  (M0 is
+// reserved: the compiler keeps nothing in it.)
+template <int LDS>
+MOE_DEV void dma16_if(int on, const void *base, uint32_t off, uint32_t lds) {
+  asm volatile(
+      "s_add_u32 m0, %2, %4\n\t"
+      "s_cmp_lg_u32 %3, 0\n\t"
+      "s_cselect_b64 exec, -1, 0\n\t"
+      "global_load_lds_dwordx4 %0, %1\n\t"
+      "s_mov_b64 exec, -1"
+      :
+      : "v"(off), "s"(base), "s"(lds), "s"(on), "n"(LDS)
+      : "memory", "scc");
+}
 MOE_DEV void dma_wait_all() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// f(integral_constant<D>) for D = BEGIN .. END - 1
+template <int BEGIN, int END, class F>
+MOE_DEV void static_for(F f) {
+  if constexpr (BEGIN < END) {
+    f(std::integral_constant<int, BEGIN>{});
+    static_for<BEGIN + 1, END>(f);
+  }
+}
 
 MOE_DEV uint32_t lds_byte(const void *p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void *)p));

@@ -13,8 +13,6 @@
 // Up to 256 tokens the weights' stream bounds the call: workgroups of 16 or 32 output
 // columns, K split over eight wavefronts, no LDS on the way in.  Above, tiles of up to
 // 256 x 256 from double-buffered LDS, filled by DMA loads.
-#include <type_traits>
-
 #include "project.h"
 
 namespace moe {
@@ -386,17 +384,22 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
   if ((int)(blockIdx.x >> 3) >= share || L >= total) return;
   const int g8 = L / (8 * tiles_n), in_g = L - g8 * 8 * tiles_n;
   const int gm = min(8, tiles_m - g8 * 8);
-  const int t0 = (g8 * 8 + in_g % gm) * BM, n0 = (in_g / gm) * BN;
+  const int t0 = __builtin_amdgcn_readfirstlane((g8 * 8 + in_g % gm) * BM);
+  const int n0 = __builtin_amdgcn_readfirstlane((in_g / gm) * BN);
   const int K = P.K, N = P.N;
   const PoolView &pool = P.pool;
 
   // byte offsets of this thread's chunks from the step's base addresses
   uint32_t a_off[A_IT], b_off[B_IT];
-  int a_k[A_IT], b_k[B_IT];  // reduction index of the chunk inside a step (NN: of its row)
+  // reduction index of chunk i of this thread inside a step (NN: of its row of B)
+  auto a_k = [&](int i) MOE_INLINE {
+    const int q = i * NT + tid;
+    return ((q & 7) ^ ((q >> 3) & 7)) * 8;
+  };
+  auto b_k = [&](int i) MOE_INLINE { return NN ? (i * NT + tid) / BCH : a_k(i); };
 #pragma unroll
   for (int i = 0; i < A_IT; ++i) {
     const int q = i * NT + tid, r = q >> 3, c = (q & 7) ^ (r & 7);
-    a_k[i] = c * 8;
     a_off[i] = ((uint32_t)min(r, P.T - 1 - t0) * (uint32_t)P.ldx + c * 8) * 2u;
   }
 #pragma unroll
@@ -404,11 +407,9 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
     const int q = i * NT + tid;
     if constexpr (!NN) {
       const int r = q >> 3, c = (q & 7) ^ (r & 7);
-      b_k[i] = c * 8;
       b_off[i] = ((uint32_t)min(r, N - 1 - n0) * (uint32_t)K + c * 8) * 2u;
     } else {
       const int r = q / BCH, c = (q % BCH) ^ ((((r & 3) | ((r >> 1) & 4)) & SWZ) << 1);
-      b_k[i] = r;
       b_off[i] = ((uint32_t)r * (uint32_t)N + (uint32_t)min(c * 8, N - 8 - n0)) * 2u;
     }
   }
@@ -430,10 +431,10 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
     const char *bb = reinterpret_cast<const char *>(NN ? b_base + (size_t)k0 * N : b_base + k0);
 #pragma unroll
     for (int i = 0; i < A_IT; ++i)
-      dma16(k0 + a_k[i] < K ? ab + a_off[i] : reinterpret_cast<const char *>(kZeroChunk), a_lds[buf] + i * NT * 16);
+      dma16(k0 + a_k(i) < K ? ab + a_off[i] : reinterpret_cast<const char *>(kZeroChunk), a_lds[buf] + i * NT * 16);
 #pragma unroll
     for (int i = 0; i < B_IT; ++i)
-      dma16(k0 + b_k[i] < K ? bb + b_off[i] : reinterpret_cast<const char *>(kZeroChunk), b_lds[buf] + i * NT * 16);
+      dma16(k0 + b_k(i) < K ? bb + b_off[i] : reinterpret_cast<const char *>(kZeroChunk), b_lds[buf] + i * NT * 16);
   };
   // ranks [r0, r0 + 64) of one adapter
   auto issue_ext = [&](int buf, int slot, int r0, int rank) MOE_INLINE {
@@ -441,8 +442,8 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
 #pragma unroll
     for (int i = 0; i < A_IT; ++i) {
       const int r = (i * NT + tid) >> 3;
-      const bool on = r0 + a_k[i] < rank && s_slot[r] == slot;
-      dma16(on ? reinterpret_cast<const char *>(P.ext_a + (size_t)(t0 + r) * pool.R + r0 + a_k[i]) : z,
+      const bool on = r0 + a_k(i) < rank && s_slot[r] == slot;
+      dma16(on ? reinterpret_cast<const char *>(P.ext_a + (size_t)(t0 + r) * pool.R + r0 + a_k(i)) : z,
             a_lds[buf] + i * NT * 16);
     }
 #pragma unroll
@@ -450,12 +451,12 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
       const char *src = z;
       if constexpr (!NN) {
         const int n = n0 + ((i * NT + tid) >> 3);
-        if (r0 + b_k[i] < rank && n < N)
-          src = reinterpret_cast<const char *>(P.ext_b + ((size_t)slot * N + n) * pool.R + r0 + b_k[i]);
+        if (r0 + b_k(i) < rank && n < N)
+          src = reinterpret_cast<const char *>(P.ext_b + ((size_t)slot * N + n) * pool.R + r0 + b_k(i));
       } else {
-        const int q = i * NT + tid, c = (q % BCH) ^ ((((b_k[i] & 3) | ((b_k[i] >> 1) & 4)) & SWZ) << 1);
-        if (r0 + b_k[i] < rank && n0 + c * 8 < N)
-          src = reinterpret_cast<const char *>(P.ext_b + ((size_t)slot * pool.R + r0 + b_k[i]) * N + n0 + c * 8);
+        const int q = i * NT + tid, c = (q % BCH) ^ ((((b_k(i) & 3) | ((b_k(i) >> 1) & 4)) & SWZ) << 1);
+        if (r0 + b_k(i) < rank && n0 + c * 8 < N)
+          src = reinterpret_cast<const char *>(P.ext_b + ((size_t)slot * pool.R + r0 + b_k(i)) * N + n0 + c * 8);
       }
       dma16(src, b_lds[buf] + i * NT * 16);
     }
@@ -497,8 +498,9 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
   // Pipeline of a step: its first half's operands are in registers when it begins; the
   // second half's are read among the first half's products, then the next step's data must
   // have landed (one barrier: also every wavefront has left this buffer), and the DMA of the
-  // step after it goes out into this buffer, among the second half's products, with the
-  // reads of the next step's first operands.
+  // step after it goes out into this buffer among the second half's products, with the reads
+  // of the next step's first operands.  (DMA loads in one burst instead held the products
+  // up: 8192 x 2048 -> 4096 in 137 us against 129, dx of 4096 x 4096 -> 2048 in 69 against 61.)
   const int steps = (K + 63) / 64, full = K / 64;
   const int chunks = (pool.R + 63) / 64;  // 64-rank chunks per adapter
   int exts = 0;                           // known once the adapters are listed
@@ -528,31 +530,54 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
 #pragma unroll
   for (int c = 0; c < kReads; ++c) read(0, 0, c, af0, bf0);
 
-  // products of one half among the reads of (buf, kk)
-  auto half = [&](u32x4_t(&af)[FM], u32x4_t(&bf)[FN], int buf, int kk, u32x4_t(&an)[FM], u32x4_t(&bn)[FN]) MOE_INLINE {
+  // the g-th of SEG shares of a full step's DMA loads
+  auto dma_one = [&](auto dc, int dbuf, const uint16_t *ab, const uint16_t *bb, int live) MOE_INLINE {
+    constexpr int d = decltype(dc)::value;
+    if constexpr (d < A_IT)
+      dma16_if<d * NT * 16>(live, ab, a_off[d], a_lds[dbuf]);
+    else
+      dma16_if<(d - A_IT) * NT * 16>(live, bb, b_off[d - A_IT], b_lds[dbuf]);
+  };
+  // products of one half among the reads of (buf, kk); with dma, also among the DMA loads at
+  // k0 into dbuf
+  auto half = [&](u32x4_t(&af)[FM], u32x4_t(&bf)[FN], int buf, int kk, u32x4_t(&an)[FM], u32x4_t(&bn)[FN], auto dma,
+                  int dbuf, int k0, int live) MOE_INLINE {
+    constexpr bool kDma = decltype(dma)::value;
+    constexpr int SEG = kDma ? 8 : 1;  // pieces that the scheduler keeps in order
+    const uint16_t *ab = a_base + k0;
+    const uint16_t *bb = NN ? b_base + (size_t)k0 * N : b_base + k0;
     __builtin_amdgcn_sched_barrier(0);
+    static_for<0, SEG>([&](auto gc) MOE_INLINE {
+      constexpr int g = decltype(gc)::value;
+      if constexpr (kDma)
+        static_for<g * (A_IT + B_IT) / SEG, (g + 1) * (A_IT + B_IT) / SEG>(
+            [&](auto dc) MOE_INLINE { dma_one(dc, dbuf, ab, bb, live); });
 #pragma unroll
-    for (int c = 0; c < kReads; ++c) read(buf, kk, c, an, bn);
+      for (int c = g * kReads / SEG; c < (g + 1) * kReads / SEG; ++c) read(buf, kk, c, an, bn);
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
+      for (int m = g * FM * FN / SEG; m < (g + 1) * FM * FN / SEG; ++m)
+        acc[m / FN][m % FN] = mfma_16x16x32(bf[m % FN], af[m / FN], acc[m / FN][m % FN]);
 #pragma unroll
-      for (int j = 0; j < FN; ++j) acc[i][j] = mfma_16x16x32(bf[j], af[i], acc[i][j]);
-#pragma unroll
-    for (int c = 0; c < kReads; ++c) {  // an LDS read, then a share of the products
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x008, FM * FN / kReads, 0);
-    }
-    __builtin_amdgcn_sched_barrier(0);
+      for (int c = 0; c < kReads / SEG; ++c) {  // an LDS read, then a share of the products
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, FM * FN / kReads, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
   };
   // (two steps to an iteration and the branches of issue() between the halves: with both
   // halves in one basic block, or one step to an iteration, the register allocator moved
   // accumulators about on every step)
   auto main_step = [&](int buf, int s) MOE_INLINE {
-    half(af0, bf0, buf, 1, af1, bf1);
+    half(af0, bf0, buf, 1, af1, bf1, std::false_type{}, 0, 0, 0);
     dma_wait_all();
     __syncthreads();
-    issue(buf, s + 2);
-    half(af1, bf1, buf ^ 1, 0, af0, bf0);  // (past the last step the reads bring what nothing uses)
+    int left = s + 2 - full;
+    asm volatile("" : "+v"(left));
+    const int more = (int)((uint32_t)__builtin_amdgcn_readfirstlane(left) >> 31);
+    if (!more) issue(buf, s + 2);
+    // (past the last step the reads bring what nothing uses)
+    half(af1, bf1, buf ^ 1, 0, af0, bf0, std::true_type{}, buf, more * (s + 2) * 64, more);
   };
 #pragma unroll 1
   for (int s = 0; s < steps; s += 2) {
@@ -582,7 +607,7 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
         for (int c = 0; c < 8; ++c) {
           const uint32_t half_mask = c & 1 ? 0xffff0000u : 0x0000ffffu;
           // (NN = 0: ranks past the adapter's, whatever the pool holds there)
-          const bool past = !NN && b_k[i] + c >= left;
+          const bool past = !NN && b_k(i) + c >= left;
           const bool bad = (v[c >> 1] & half_mask & 0x7f807f80u) == (half_mask & 0x7f807f80u);
           odd |= bad && !past;
           change |= bad || past;
