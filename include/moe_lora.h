@@ -189,8 +189,8 @@ int moe_lora_route(const moe_lora_dims *dims, int routing, const moe_lora_groupe
  * in range.
  * Limits: num_tokens <= 65536 (MOE_LORA_ERR_UNSUPPORTED; route larger batches in chunks).
  * dims: num_tokens, num_experts and top_k are used (hidden and inter only checked).
- * Workspace: moe_lora_route_scored_workspace_size bytes (0 up to 64 tokens: one launch;
- * larger batches take two). */
+ * Workspace: moe_lora_route_scored_workspace_size bytes (0 where the batch takes one launch:
+ * up to 64 tokens, or 16 with a bias or groups scored by two; larger batches take two). */
 typedef enum { MOE_LORA_SCORE_SOFTMAX = 0, MOE_LORA_SCORE_SIGMOID = 1 } moe_lora_score;
 typedef enum { MOE_LORA_DTYPE_BF16 = 0, MOE_LORA_DTYPE_F32 = 1 } moe_lora_dtype;
 

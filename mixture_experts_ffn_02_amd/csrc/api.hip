@@ -177,7 +177,8 @@ int check_groups(const moe_lora_dims *d, const moe_lora_scoring *sc) {
 
 size_t moe_lora_route_scored_workspace_size(const moe_lora_dims *d, const moe_lora_scoring *sc) {
   if (check_scoring(d, sc) != MOE_LORA_OK || check_groups(d, sc) != MOE_LORA_OK || d->num_tokens == 0) return 0;
-  return moe::scored_workspace_bytes(d->num_tokens, d->num_experts, d->top_k, sc->n_group > 1);
+  return moe::scored_workspace_bytes(d->num_tokens, d->num_experts, d->top_k, sc->n_group > 1,
+                                     moe::scored_wide(sc->bias != nullptr, sc->n_group, sc->group_score));
 }
 
 int moe_lora_route_scored(const moe_lora_dims *d, const moe_lora_scoring *sc, const void *logits,
@@ -193,7 +194,7 @@ int moe_lora_route_scored(const moe_lora_dims *d, const moe_lora_scoring *sc, co
   if (!logits || !topk_ids || !topk_weights || !e2p || !p2e || !aligned16(logits) || !aligned16(topk_ids) ||
       !aligned16(topk_weights) || !aligned16(e2p) || !aligned16(p2e))
     return MOE_LORA_ERR_INVALID_ARGUMENT;
-  const size_t need = moe::scored_workspace_bytes(d->num_tokens, E, d->top_k, sc->n_group > 1);
+  const size_t need = moe_lora_route_scored_workspace_size(d, sc);
   if (ws_bytes < need) return MOE_LORA_ERR_WORKSPACE_TOO_SMALL;
   if (need > 0 && (!ws || !aligned16(ws))) return MOE_LORA_ERR_INVALID_ARGUMENT;
   moe::RouteArgs a{};

@@ -48,7 +48,8 @@ struct ScoredBackwardArgs {
   bool f32, renormalize;
   float scale;
 };
-size_t scored_workspace_bytes(int T, int E, int K, bool groups);
+bool scored_wide(bool bias, int n_group, int group_score);  // whether keys are scores
+size_t scored_workspace_bytes(int T, int E, int K, bool groups, bool wide);
 int scored_max_tokens();
 // RouteArgs: logits (either type), sizes, groups and outputs; method, rsf and bias unused
 int launch_route_scored(const RouteArgs &a, const ScoredArgs &s, hipStream_t st);

@@ -365,12 +365,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_finish_kernel(RouteParams
       const int e = lane * per_lane + q;
       local += (e < E) ? tot[e] : 0;
     }
-    int incl = local;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int o = __shfl_up(incl, off);
-      if (lane >= off) incl += o;
-    }
+    const int incl = wave_scan_add(local);
     int run = incl - local;
     for (int q = 0; q < per_lane; ++q) {
       const int e = lane * per_lane + q;

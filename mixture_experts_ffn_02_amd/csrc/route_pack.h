@@ -16,6 +16,18 @@ struct RouteParams {
   int num_wg;
 };
 
+// inclusive sum over the lanes of a wavefront: shifts inside the 16-lane rows, then row ends
+// into the rows above (no LDS round trip per step)
+MOE_DEV int wave_scan_add(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);  // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31 into rows 2 and 3
+  return v;
+}
+
 // Second launch of a multi-workgroup batch (route_finish_kernel): block-relative positions
 // become final ones.
 int launch_route_finish(const RouteParams &P, hipStream_t s);
@@ -48,12 +60,7 @@ MOE_DEV void pack_block(const RouteArgs &a, int32_t *hist_w, const int32_t *ids_
       const int e = lane * per_lane + q;
       local += (e < E) ? tot[e] : 0;
     }
-    int incl = local;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int o = __shfl_up(incl, off);
-      if (lane >= off) incl += o;
-    }
+    const int incl = wave_scan_add(local);
     int run = incl - local;
     for (int q = 0; q < per_lane; ++q) {
       const int e = lane * per_lane + q;

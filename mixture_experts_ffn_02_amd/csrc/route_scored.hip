@@ -7,14 +7,18 @@
 // that one instruction stream selects for four tokens.  Each lane holds EPL consecutive
 // experts as order-preserving unsigned keys (0 = not selectable), so a selection step is
 // a local max, a max over the lanes and a ballot; equal keys go to the lowest lane, which
-// holds the lowest index.  Biased keys are made and compared in fp64 (as two 32-bit words;
-// the low words are only looked at when the high words of two experts are equal), so that
-// near-ties resolve as the definition does.  The weights are fp32, from the log scores
-// relative to the largest chosen one when renormalised (nothing underflows in the sum).
-// The expert-sorted pack is the one of moe_lora_route.
+// holds the lowest index.  Keys with a bias, and groups scored by two, are defined in fp64:
+// a first choice is made on their fp32 values, whose error is known, and stands if every
+// difference that decided something is larger than two such errors; else (about one token
+// in some hundreds, and exact ties) the token is chosen again on fp64 keys, as two 32-bit
+// words.  The weights are fp32, from the log scores relative to the largest chosen one when
+// renormalised (nothing underflows in the sum).  The expert-sorted pack is the one of
+// moe_lora_route.
 //
 // Bound: at 1 to 64 tokens one workgroup's latency (one launch); above, the selection's
 // vector instructions (two launches).
+#include <type_traits>
+
 #include "common.h"
 #include "kernels.h"
 #include "route_pack.h"
@@ -23,19 +27,30 @@ namespace moe {
 namespace {
 
 constexpr int kScoredOneWg = 64;     // batches up to this run in one workgroup and one launch
+constexpr int kScoredOneWgWide = 16; // the same with keys of fp64
 constexpr int kScoredMaxTok = 256;   // tokens of one workgroup (its ids live in LDS)
 
+template <int CTRL>
+MOE_DEV uint32_t dpp_max(uint32_t v) {
+  const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xF, 0xF, false);
+  return o > v ? o : v;
+}
+// max over the LPT lanes of a token, in all of them: quad swaps, rotations by 4 and 8 inside
+// the 16-lane rows, then (64 lanes) rows 0 and 2 into their neighbours, row 1 into the upper
+// half, and the last lane's value to all.  (The runtime's wave reduction walks the lanes one
+// by one: a selection step took 0.47 us with it.)
 template <int LPT>
 MOE_DEV uint32_t lanes_max_u32(uint32_t v) {
-  if constexpr (LPT == 64) return __reduce_max_sync(~0ull, v);
-  uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false);  // xor 1
-  v = o > v ? o : v;
-  o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false);  // xor 2
-  v = o > v ? o : v;
-  o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xF, 0xF, false);  // row_ror 4
-  v = o > v ? o : v;
-  o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xF, 0xF, false);  // row_ror 8
-  return o > v ? o : v;
+  v = dpp_max<0xB1>(v);
+  v = dpp_max<0x4E>(v);
+  v = dpp_max<0x124>(v);
+  v = dpp_max<0x128>(v);
+  if constexpr (LPT == 64) {
+    v = dpp_max<0x142>(v);  // row_bcast:15
+    v = dpp_max<0x143>(v);  // row_bcast:31
+    v = (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+  }
+  return v;
 }
 
 template <int CTRL>
@@ -82,15 +97,15 @@ MOE_DEV float lanes_max(float v) {
   return key_f32(lanes_max_u32<LPT>(v != v ? 1u : f32_key(v)));
 }
 
-// One selection step: the largest key among this token's lanes (ties to the lowest index).
+// One selection step: the largest key m among this token's lanes (ties to the lowest index).
 // Returns true in the one lane that owns it, with its local index; that key is cleared.
-// lower: the ballot bits of the token's lanes below this one.
+// lanes, lower: the ballot bits of the token's lanes, and of those below this one.
 template <int LPT, int N, bool WIDE>
-MOE_DEV bool take_best(uint32_t (&hi)[N], uint32_t (&lo)[N], uint64_t lanes, uint64_t lower, int &at) {
+MOE_DEV bool take_best(uint32_t (&hi)[N], uint32_t (&lo)[N], uint64_t lanes, uint64_t lower, uint32_t &m, int &at) {
   uint32_t best = hi[0];
 #pragma unroll
   for (int i = 1; i < N; ++i) best = hi[i] > best ? hi[i] : best;
-  const uint32_t m = lanes_max_u32<LPT>(best);
+  m = lanes_max_u32<LPT>(best);
   bool mine = best == m;
   uint64_t who = __ballot(mine) & lanes;
   uint32_t ml = 0;
@@ -103,26 +118,75 @@ MOE_DEV bool take_best(uint32_t (&hi)[N], uint32_t (&lo)[N], uint64_t lanes, uin
       uint32_t bl = 0;
 #pragma unroll
       for (int i = 0; i < N; ++i) bl = (hi[i] == m && lo[i] > bl) ? lo[i] : bl;
-      ml = lanes_max_u32<LPT>(bl);
+      ml = lanes_max_u32<LPT>(mine ? bl : 0u);
       mine = mine && bl == ml;
       who = __ballot(mine) & lanes;
       by_low = true;
     }
   }
-  if (!mine || (who & lower) != 0) return false;
-  bool open = true;
+  if constexpr (LPT == 64) {
+    // no branch: the owner is one lane of the wavefront
+    const bool own = lane_id() == __builtin_ctzll(who | (1ull << 63));
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const bool hit = open && hi[i] == m && (!WIDE || !by_low || lo[i] == ml);
-    at = hit ? i : at;
-    hi[i] = hit ? 0u : hi[i];
-    open = open && !hit;
+    for (int i = N - 1; i >= 0; --i) at = hi[i] == m && (!WIDE || !by_low || lo[i] == ml) ? i : at;
+#pragma unroll
+    for (int i = 0; i < N; ++i) hi[i] = own && at == i ? 0u : hi[i];
+    return own;
   }
+  if (!mine || (who & lower) != 0) return false;
+#pragma unroll
+  for (int i = N - 1; i >= 0; --i) at = hi[i] == m && (!WIDE || !by_low || lo[i] == ml) ? i : at;
+#pragma unroll
+  for (int i = 0; i < N; ++i) hi[i] = at == i ? 0u : hi[i];
   return true;
+}
+
+// Whether fp32 keys a >= b (order keys of values) decide as the fp64 ones do: scores are off
+// by at most 2^-20 (exp, a sum of up to 512 terms and a division in fp32 around values of at
+// most 1: some 16 half steps of 2^-24), a key by a half step of itself more, a group's sum of
+// two by twice that.  Ties and what is not finite are not decided.
+MOE_DEV bool decided(uint32_t a, uint32_t b) {
+  const float x = key_f32(a), y = key_f32(b);
+  return x - y > 0x1p-17f + 0x1p-20f * fmaxf(fabsf(x), fabsf(y)) && fabsf(x) < 1e30f;
+}
+
+// orders one wavefront's own LDS writes and reads
+MOE_DEV void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 MOE_DEV float load_logit(const void *p, size_t i, bool f32) {
   return f32 ? static_cast<const float *>(p)[i] : bf16_to_f32(static_cast<const uint16_t *>(p)[i]);
+}
+
+// N consecutive logits of a row from expert e0 (-inf past the last): whole vectors where every
+// lane's run starts aligned and ends inside the row, else one by one (which takes the
+// address path one lane a cycle)
+template <int N>
+MOE_DEV void load_logits(const void *p, size_t row, int e0, int E, bool f32, float (&x)[N]) {
+  if (N > 1 && E % N == 0) {
+    if (e0 >= E) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = -INFINITY;
+    } else if (f32) {
+      constexpr int V = N < 4 ? N : 4;
+      typedef float vec __attribute__((ext_vector_type(V)));
+      const vec *v = reinterpret_cast<const vec *>(static_cast<const float *>(p) + row + e0);
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = v[i / V][i % V];
+    } else {
+      constexpr int V = N < 8 ? N : 8;
+      typedef uint16_t vec __attribute__((ext_vector_type(V)));
+      const vec *v = reinterpret_cast<const vec *>(static_cast<const uint16_t *>(p) + row + e0);
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = bf16_to_f32(v[i / V][i % V]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = e0 + i < E ? load_logit(p, row + e0 + i, f32) : -INFINITY;
+  }
 }
 
 MOE_DEV float log_sigmoid(float x) { return fminf(x, 0.f) - log1pf(expf(-fabsf(x))); }
@@ -133,7 +197,7 @@ struct ScoredParams {
 };
 
 // LDS (dynamic): hist [waves][E] int | tot [E] | wgbase [E] | ids [tokens][K] int
-//                | chosen logits [waves][64 / LPT][K] float | group keys [waves][E] double (groups)
+//                | group keys [waves][E] double (groups)
 template <int LPT, int EPL, bool WIDE, bool MULTI>
 __global__ __launch_bounds__(kRouteThreads) void scored_kernel(const ScoredParams P) {
   const RouteArgs &a = P.r.a;
@@ -146,9 +210,8 @@ __global__ __launch_bounds__(kRouteThreads) void scored_kernel(const ScoredParam
   int32_t *tot = hist_w + waves * E;
   int32_t *wgbase = tot + E;
   int32_t *ids_l = wgbase + E;
-  float *lg_l = reinterpret_cast<float *>(ids_l + P.r.tok_per_wg * K);
   double *grp = reinterpret_cast<double *>(
-      smem + (((size_t)(waves * E + 2 * E + P.r.tok_per_wg * K + waves * TPW * K) * 4 + 15) & ~(size_t)15));
+      smem + (((size_t)(waves * E + 2 * E + P.r.tok_per_wg * K) * 4 + 15) & ~(size_t)15));
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int sub = lane / LPT, ll = lane % LPT;
@@ -161,7 +224,6 @@ __global__ __launch_bounds__(kRouteThreads) void scored_kernel(const ScoredParam
   const int w_end = min(t_end, w_begin + tpw);
   const uint64_t lanes = LPT == 64 ? ~0ull : (0xffffull << (lane & 48));
   const uint64_t lower = lanes & ((1ull << lane) - 1);
-  float *lg_w = lg_l + (wave * TPW + sub) * K;
   const bool sigmoid = s.score == MOE_LORA_SCORE_SIGMOID;
   const bool grouped = LPT == 64 && a.n_group > 1;  // (groups run on whole wavefronts)
 
@@ -171,119 +233,164 @@ __global__ __launch_bounds__(kRouteThreads) void scored_kernel(const ScoredParam
     int32_t *id_row = ids_l + (t - t_begin) * K;
     float x[EPL];
     const size_t row = (size_t)t * E;
+    load_logits<EPL>(a.logits, row, ll * EPL, E, s.f32, x);
+    float bias[WIDE ? EPL : 1];
+    if constexpr (WIDE) {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = ll * EPL + i;
-      x[i] = e < E ? load_logit(a.logits, row + e, s.f32) : -INFINITY;
+      for (int i = 0; i < EPL; ++i) bias[i] = s.bias && ll * EPL + i < E ? s.bias[ll * EPL + i] : 0.f;
     }
-    // softmax over all experts: largest logit and sum (weights without renormalisation)
-    float mx = 0.f, total = 0.f;
+    // softmax over all experts: largest logit and sum
+    float mx = 0.f, total = 1.f;
+    float px[EPL];
     if (!sigmoid && (!s.renormalize || WIDE)) {
       float m = x[0];
 #pragma unroll
       for (int i = 1; i < EPL; ++i) m = fmaxf(m, x[i]);
       mx = lanes_max<LPT>(m);
       if (mx == -INFINITY) mx = 0.f;  // every expert masked
-      if (!s.renormalize) {
+      total = 0.f;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) total += (ll * EPL + i < E) ? expf(x[i] - mx) : 0.f;
-        total = lanes_sum<LPT>(total);
+      for (int i = 0; i < EPL; ++i) {
+        px[i] = expf(x[i] - mx);
+        total += ll * EPL + i < E ? px[i] : 0.f;
       }
+      total = lanes_sum<LPT>(total);
+      total = total == 0.f ? 1.f : total;
     }
-    uint32_t hi[EPL], lo[EPL];
-    if constexpr (WIDE) {
-      double p[EPL], sum = 0.0;
+
+    int chosen = 0;  // LPT = 64: lane j's j-th expert
+    // The choice on keys of 32 bits, or (exact) of 64 where WIDE.  Returns whether it stands.
+    auto choose = [&](auto exact) __attribute__((always_inline)) {
+      constexpr bool F64 = decltype(exact)::value;
+      bool sure = true;
+      uint32_t hi[EPL], lo[EPL];
+      float gk32[EPL];
+      if constexpr (F64) {
+        double p[EPL], sum = 0.0;
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        const bool in = ll * EPL + i < E;
-        p[i] = in ? (sigmoid ? 1.0 / (1.0 + exp(-(double)x[i])) : exp((double)x[i] - (double)mx)) : 0.0;
-        sum += p[i];
-      }
-      if (!sigmoid) {
-        sum = lanes_sum_f64<LPT>(sum);
-        sum = sum == 0.0 ? 1.0 : sum;
-      }
+        for (int i = 0; i < EPL; ++i) {
+          const bool in = ll * EPL + i < E;
+          p[i] = in ? (sigmoid ? 1.0 / (1.0 + exp(-(double)x[i])) : exp((double)x[i] - (double)mx)) : 0.0;
+          sum += p[i];
+        }
+        if (!sigmoid) {
+          sum = lanes_sum_f64<LPT>(sum);
+          sum = sum == 0.0 ? 1.0 : sum;
+        }
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        const int e = ll * EPL + i;
-        double key = sigmoid ? p[i] : p[i] / sum;
-        if (s.bias) key += e < E ? (double)s.bias[e] : 0.0;
-        if (grouped && e < E) grp[wave * E + e] = key;
-        // without a bias only the groups need the scores: experts compare by logit
-        const uint64_t k = s.bias ? f64_key(key) : (uint64_t)f32_key(x[i]) << 32;
-        hi[i] = e < E ? (uint32_t)(k >> 32) : 0u;
-        lo[i] = e < E ? (uint32_t)k : 0u;
-      }
-    } else {
+        for (int i = 0; i < EPL; ++i) {
+          const int e = ll * EPL + i;
+          const double key = (sigmoid ? p[i] : p[i] / sum) + (double)bias[i];
+          if (grouped && e < E) grp[wave * E + e] = key;
+          // without a bias only the groups need the scores: experts compare by logit
+          const uint64_t k = s.bias ? f64_key(key) : (uint64_t)f32_key(x[i]) << 32;
+          hi[i] = e < E ? (uint32_t)(k >> 32) : 0u;
+          lo[i] = e < E ? (uint32_t)k : 0u;
+        }
+      } else {
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        const int e = ll * EPL + i;
-        hi[i] = e < E ? f32_key(x[i]) : 0u;
-        lo[i] = 0u;
-        if (grouped && e < E) grp[wave * E + e] = (double)x[i];
-      }
-    }
-    if (grouped) {
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-      // lanes split over the groups, then joined: lpg lanes (a power of two) scan a group
-      const int per = E / a.n_group;
-      int lpg = 1;
-      while (lpg * 2 * a.n_group <= 64 && lpg < per) lpg *= 2;
-      const int g = lane / lpg;
-      double b0 = -INFINITY, b1 = -INFINITY;
-      if (g < a.n_group) {
-        for (int q = lane % lpg; q < per; q += lpg) {
-          const double v = grp[wave * E + g * per + q];
-          if (v > b0 || v != v) {
-            b1 = b0;
-            b0 = v;
-          } else if (v > b1) {
-            b1 = v;
-          }
+        for (int i = 0; i < EPL; ++i) {
+          const int e = ll * EPL + i;
+          gk32[i] = x[i];
+          if constexpr (WIDE) gk32[i] = (sigmoid ? 1.f / (1.f + expf(-x[i])) : px[i] / total) + bias[i];
+          hi[i] = e < E ? f32_key(WIDE && s.bias ? gk32[i] : x[i]) : 0u;
+          lo[i] = 0u;
+          if (grouped && e < E) grp[wave * E + e] = (double)gk32[i];
         }
       }
-      for (int m = 1; m < lpg; m <<= 1) {
-        const double o0 = __shfl_xor(b0, m), o1 = __shfl_xor(b1, m);
-        const bool up = o0 > b0 || o0 != o0;
-        b1 = up ? (b0 > o1 ? b0 : o1) : (b1 > o0 ? b1 : o0);
-        b0 = up ? o0 : b0;
-      }
-      double gv = (s.group_score == 2 && per > 1) ? b0 + b1 : b0;
-      const bool head = g < a.n_group && lane % lpg == 0;
-      const uint64_t gk = f64_key(gv);
-      uint32_t gh[1] = {head ? (uint32_t)(gk >> 32) : 0u}, gl[1] = {(uint32_t)gk};
-      uint64_t kept = 0;
-      for (int r = 0; r < a.topk_group; ++r) {
+      if (grouped) {
+        wave_lds_order();
+        // lanes split over the groups, then joined: lpg lanes (a power of two) scan a group
+        const int per = E / a.n_group;
+        int lpg = 1;
+        while (lpg * 2 * a.n_group <= 64 && lpg < per) lpg *= 2;
+        const int g = lane / lpg;
+        double b0 = -INFINITY, b1 = -INFINITY;
+        if (g < a.n_group) {
+          for (int q = lane % lpg; q < per; q += lpg) {
+            const double v = grp[wave * E + g * per + q];
+            if (v > b0 || v != v) {
+              b1 = b0;
+              b0 = v;
+            } else if (v > b1) {
+              b1 = v;
+            }
+          }
+        }
+        for (int m = 1; m < lpg; m <<= 1) {
+          const double o0 = __shfl_xor(b0, m), o1 = __shfl_xor(b1, m);
+          const bool up = o0 > b0 || o0 != o0;
+          b1 = up ? (b0 > o1 ? b0 : o1) : (b1 > o0 ? b1 : o0);
+          b0 = up ? o0 : b0;
+        }
+        const double gv = (s.group_score == 2 && per > 1) ? b0 + b1 : b0;
+        const bool head = g < a.n_group && lane % lpg == 0;
+        uint64_t kept = 0;
+        uint32_t m = 0;
         int at = 0;
-        const bool own = take_best<64, 1, true>(gh, gl, ~0ull, (1ull << lane) - 1, at);
-        kept |= __ballot(own);  // bit of the group's first lane
-      }
+        uint32_t gh[1], gl[1] = {0u};
+        if constexpr (F64) {
+          const uint64_t gk = f64_key(gv);
+          gh[0] = head ? (uint32_t)(gk >> 32) : 0u;
+          gl[0] = (uint32_t)gk;
+        } else {
+          gh[0] = head ? f32_key((float)gv) : 0u;  // (a sum of two fp32 keys: one more half step)
+        }
+        for (int r = 0; r < a.topk_group; ++r)
+          kept |= __ballot(take_best<64, 1, F64>(gh, gl, ~0ull, (1ull << lane) - 1, m, at));  // the groups' first lanes
+        if constexpr (WIDE && !F64) {
+          if (a.topk_group < a.n_group) sure = decided(m, lanes_max_u32<64>(gh[0]));
+        }
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        const int e = ll * EPL + i;
-        const int ge = e < E ? e / per : 0;
-        if (!((kept >> (ge * lpg)) & 1ull)) hi[i] = 0u;
+        for (int i = 0; i < EPL; ++i) {
+          const int e = ll * EPL + i;
+          const int ge = e < E ? e / per : 0;
+          if (!((kept >> (ge * lpg)) & 1ull)) hi[i] = 0u;
+        }
+        __builtin_amdgcn_wave_barrier();
       }
-      __builtin_amdgcn_wave_barrier();
-    }
-    for (int j = 0; j < K; ++j) {
-      int at = 0;
-      if (take_best<LPT, EPL, WIDE>(hi, lo, lanes, lower, at)) {
-        float xv = x[0];
+      uint32_t last = 0;
+      for (int j = 0; j < K; ++j) {
+        int at = 0;
+        uint32_t m;
+        const bool own = take_best<LPT, EPL, F64>(hi, lo, lanes, lower, m, at);
+        if constexpr (LPT == 64) {
+          const int e = __builtin_amdgcn_readlane(ll * EPL + at, __builtin_ctzll(__ballot(own)));
+          chosen = lane == j ? e : chosen;
+        } else if (own && tv) {
+          id_row[j] = ll * EPL + at;
+        }
+        if constexpr (WIDE && !F64) {
+          if (s.bias && j > 0) sure = sure && decided(last, m);
+          last = m;
+        }
+      }
+      if constexpr (WIDE && !F64) {
+        if (s.bias) {
+          uint32_t best = hi[0];
 #pragma unroll
-        for (int i = 1; i < EPL; ++i) xv = at == i ? x[i] : xv;
-        if (tv) id_row[j] = ll * EPL + at;
-        lg_w[j] = xv;
+          for (int i = 1; i < EPL; ++i) best = hi[i] > best ? hi[i] : best;
+          best = lanes_max_u32<LPT>(best);
+          sure = sure && (best == 0u || decided(last, best));
+        }
       }
+      return sure;
+    };
+    const bool sure = choose(std::false_type{});
+    if constexpr (WIDE) {
+      if (__ballot(!sure) != 0) choose(std::true_type{});
     }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     // lane j < K of the token: its j-th expert and weight
     const bool mine = ll < K;
-    const float xc = mine ? lg_w[ll] : 0.f;
+    int id = 0;
+    if constexpr (LPT == 64) {
+      id = mine ? chosen : 0;
+      if (mine) id_row[ll] = id;
+    } else {
+      wave_lds_order();
+      id = mine ? id_row[ll] : 0;
+    }
+    const float xc = mine ? load_logit(a.logits, row + id, s.f32) : 0.f;
     float w;
     if (s.renormalize) {
       const float z = !mine ? -INFINITY : sigmoid ? log_sigmoid(xc) : xc;
@@ -295,13 +402,12 @@ __global__ __launch_bounds__(kRouteThreads) void scored_kernel(const ScoredParam
     } else if (sigmoid) {
       w = 1.f / (1.f + expf(-xc));
     } else {
-      w = expf(xc - mx) / (total == 0.f ? 1.f : total);
+      w = expf(xc - mx) / total;
     }
     if (mine && tv) {
-      const int e = id_row[ll];
-      a.ids[(size_t)t * K + ll] = e;
+      a.ids[(size_t)t * K + ll] = id;
       a.weights[(size_t)t * K + ll] = s.scale * w;
-      atomicAdd(&hist_w[wave * E + e], 1);
+      atomicAdd(&hist_w[wave * E + id], 1);
     }
     __builtin_amdgcn_wave_barrier();
   }
@@ -406,13 +512,9 @@ __global__ __launch_bounds__(256) void scored_backward_kernel(const ScoredBackwa
       if (j < ll) first = false;
     }
   }
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  wave_lds_order();
   if (first) at[id] = sum_g;
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  wave_lds_order();
   float d[CH][VEC];
   float dot = 0.f;
 #pragma unroll
@@ -458,12 +560,15 @@ struct Plan {
 
 // Lanes per token: groups take a whole wavefront (their keys' LDS rows, one per wave, would
 // not fit for four tokens at 512 experts), and so do k > 16 (one lane per chosen expert)
-// and batches too small to fill the device with four tokens a wave.
-Plan plan_scored(int T, int E, int K, bool groups) {
+// and batches too small to fill the device with four tokens a wave.  One workgroup and one
+// launch up to 64 tokens; up to 16 where the keys are scores, whose choice takes a wavefront
+// longer (64 tokens, 256 experts in 8 groups: 38 us in one workgroup, 19 in four and a second
+// launch).
+Plan plan_scored(int T, int E, int K, bool groups, bool wide) {
   Plan p;
   p.lpt = (groups || K > 16 || T <= 4096) ? 64 : 16;
   const int per = 64 / p.lpt;
-  if (T <= kScoredOneWg) {
+  if (T <= (wide ? kScoredOneWgWide : kScoredOneWg)) {
     p.waves = T < 16 ? T : 16;
     p.tok_per_wg = T;
     p.num_wg = 1;
@@ -477,7 +582,7 @@ Plan plan_scored(int T, int E, int K, bool groups) {
     }
     p.num_wg = n;
   }
-  p.lds = ((size_t)(p.waves * E + 2 * E + p.tok_per_wg * K + p.waves * per * K) * 4 + 15) & ~(size_t)15;
+  p.lds = ((size_t)(p.waves * E + 2 * E + p.tok_per_wg * K) * 4 + 15) & ~(size_t)15;
   if (groups) p.lds += (size_t)p.waves * E * sizeof(double);
   return p;
 }
@@ -535,23 +640,25 @@ int launch_backward(const ScoredBackwardArgs &a, hipStream_t s) {
 
 }  // namespace
 
-size_t scored_workspace_bytes(int T, int E, int K, bool groups) {
-  const Plan p = plan_scored(T, E, K, groups);
+size_t scored_workspace_bytes(int T, int E, int K, bool groups, bool wide) {
+  const Plan p = plan_scored(T, E, K, groups, wide);
   return p.num_wg > 1 ? (size_t)p.num_wg * E * sizeof(int32_t) : 0;
 }
+
+bool scored_wide(bool bias, int n_group, int group_score) { return bias || (n_group > 1 && group_score == 2); }
 
 int scored_max_tokens() { return kMaxRouteWg * kScoredMaxTok; }
 
 int launch_route_scored(const RouteArgs &a, const ScoredArgs &s, hipStream_t st) {
   const bool groups = a.n_group > 1;
-  const Plan p = plan_scored(a.T, a.E, a.K, groups);
+  // fp64 keys: where a bias or a group's sum of two compares scores
+  const bool wide = scored_wide(s.bias != nullptr, a.n_group, s.group_score);
+  const Plan p = plan_scored(a.T, a.E, a.K, groups, wide);
   ScoredParams P;
   P.r.a = a;
   P.r.tok_per_wg = p.tok_per_wg;
   P.r.num_wg = p.num_wg;
   P.s = s;
-  // fp64 keys: where a bias or a group's sum of two compares scores
-  const bool wide = s.bias || (groups && s.group_score == 2);
   const int r = p.lpt == 64 ? launch_experts<64>(P, p, wide, st) : launch_experts<16>(P, p, wide, st);
   if (r != ST_OK || p.num_wg == 1) return r;
   return launch_route_finish(P.r, st);
