@@ -93,6 +93,9 @@ struct ShrinkArgs {
   PoolView pool;
   uint16_t *out_bf16;  // [T, R]
   float *out_f32;      // [T, R] or NULL
+  // where not NULL: the tokens by adapter [T] and the adapters' first places [S + 1], made by
+  // a workgroup of the same launch
+  int32_t *order, *seg;
 };
 struct ProjectArgs {
   const uint16_t *x;  // [T, K], rows ldx apart

@@ -100,6 +100,82 @@ MOE_DEV int rank_of(const PoolView &P, int s) {
   return r < P.R ? r : P.R;
 }
 
+// The tokens with an adapter, by adapter and ascending inside one, into order; where each
+// adapter's tokens begin into seg [S + 1].  Called by one workgroup of NT threads; hist:
+// (NT / 64 + 1) * (S + 1) ints of LDS.
+template <int NT>
+MOE_DEV void order_tokens(const PoolView &P, int T, int32_t *order, int32_t *seg, int *hist) {
+  constexpr int W = NT / 64;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int n = P.S + 1;
+  int *start = hist + W * n;
+  for (int i = tid; i < W * n; i += NT) hist[i] = 0;
+  __syncthreads();
+  const int per = (T + W - 1) / W;
+  const int t0 = min(T, wave * per), t1 = min(T, t0 + per);
+  int rank;
+  for (int t = t0 + lane; t < t1; t += 64) {
+    const int s = adapter_of(P, t, rank);
+    if (s >= 0) atomicAdd(&hist[wave * n + s], 1);
+  }
+  __syncthreads();
+  for (int s = tid; s < n; s += NT) {
+    int run = 0;
+    for (int w = 0; w < W; ++w) {
+      const int c = hist[w * n + s];
+      hist[w * n + s] = run;
+      run += c;
+    }
+    start[s] = run;
+  }
+  __syncthreads();
+  if (wave == 0) {  // exclusive scan over the adapters
+    const int each = (n + 63) / 64;
+    int local = 0;
+    for (int q = 0; q < each; ++q) local += lane * each + q < n ? start[lane * each + q] : 0;
+    int incl = local;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int o = __shfl_up(incl, off);
+      if (lane >= off) incl += o;
+    }
+    int run = incl - local;
+    for (int q = 0; q < each; ++q) {
+      const int s = lane * each + q;
+      if (s < n) {
+        const int c = start[s];
+        start[s] = run;
+        seg[s] = run;
+        run += c;
+      }
+    }
+  }
+  __syncthreads();
+  int *mine = hist + wave * n;
+  int bits = 0;
+  while ((1 << bits) < P.S) ++bits;
+  const uint64_t lt = (1ull << lane) - 1;
+  for (int b = t0; b < t1; b += 64) {
+    const int t = b + lane;
+    const int s = t < t1 ? adapter_of(P, t, rank) : -1;
+    const bool on = s >= 0;
+    uint64_t peers = __ballot(on);
+    for (int q = 0; q < bits; ++q) {
+      const bool bit = on && ((s >> q) & 1);
+      const uint64_t m = __ballot(bit);
+      peers &= bit ? m : ~m;
+    }
+    int at = 0;
+    if (on) at = mine[s];
+    wave_lds_fence();
+    if (on) {
+      order[start[s] + at + __popcll(peers & lt)] = t;
+      if ((peers & lt) == 0ull) mine[s] = at + __popcll(peers);
+    }
+    wave_lds_fence();
+  }
+}
+
 // Distinct adapters of a tile's rows, thread r giving row r's (slot -1: none): row slots into
 // s_slot, the list of slot | rank << 16 in ascending order into s_list, its length returned
 // (uniform).  Called by the whole workgroup; s_bits: 16 words.

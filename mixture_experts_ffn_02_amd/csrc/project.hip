@@ -36,7 +36,15 @@ __global__ __launch_bounds__(kShrinkWaves * 64, LONG ? 3 : 2) void shrink_kernel
   __shared__ int s_slot[16];
   float *part = reinterpret_cast<float *>(smem);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int t0 = blockIdx.x * 16;
+  if (TR && P.order) {  // the first workgroup orders the tokens
+    static_assert((kShrinkWaves + 1) * (MOE_LORA_MAX_POOL_SLOTS + 1) * 4 <= sizeof(smem), "order in the stages' LDS");
+    if (blockIdx.x == 0) {
+      if (blockIdx.y == 0)
+        order_tokens<kShrinkWaves * 64>(P.pool, P.T, P.order, P.seg, reinterpret_cast<int *>(smem));
+      return;
+    }
+  }
+  const int t0 = ((int)blockIdx.x - (TR && P.order ? 1 : 0)) * 16;
   const int row = lane & 15, grp = lane >> 4;
   int rank_row = 0;
   const int t_row = t0 + row;
@@ -666,7 +674,7 @@ constexpr int kFewTokens = 256;
 
 template <bool TR, bool LONG>
 int launch_shrink_ranks(const ShrinkArgs &a, hipStream_t s) {
-  const dim3 grid((a.T + 15) / 16, LONG ? 1 : 16);
+  const dim3 grid((a.T + 15) / 16 + (TR && a.order ? 1 : 0), LONG ? 1 : 16);
   if (a.pool.R <= 16)
     shrink_kernel<1, TR, LONG><<<grid, kShrinkWaves * 64, 0, s>>>(a);
   else if (a.pool.R <= 32)
@@ -721,7 +729,7 @@ size_t project_workspace_bytes(int T, int R) { return ((size_t)T * R * 2 + 255) 
 
 int launch_project(const ProjectArgs &a, float *v, hipStream_t s) {
   if (a.pool.S > 0) {
-    const ShrinkArgs sh{a.x, a.ldx, a.T, a.K, a.a_or_b, a.pool, const_cast<uint16_t *>(a.ext_a), v};
+    const ShrinkArgs sh{a.x, a.ldx, a.T, a.K, a.a_or_b, a.pool, const_cast<uint16_t *>(a.ext_a), v, nullptr, nullptr};
     const int st = launch_shrink<false>(sh, s);
     if (st != ST_OK) return st;
   }

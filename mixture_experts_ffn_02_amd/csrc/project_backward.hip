@@ -3,9 +3,9 @@
 //   u_t = s_a B_a^T dy_t     dx_t = W^T dy_t + A_a^T u_t
 //   dA_a = sum_t u_t x_t^T   dB_a = s_a sum_t dy_t v_t^T        (t over the adapter's tokens)
 //
-// Launches: the tokens' order by adapter (one workgroup), u (the forward's shrink over B),
-// dx (the forward's tiles with transposed weight reads), dA and dB together, and their
-// parts' sums where a segment was split.  dA and dB stream x and dy once: a wavefront
+// Launches: u (the forward's shrink over B) with the tokens' order by adapter in a workgroup
+// of its own beside it, dx (the forward's tiles with transposed weight reads), dA and dB
+// together, and their parts' sums where a segment was split.  dA and dB stream x and dy once: a wavefront
 // takes 32 tokens x 128 columns as eight rows of 16 bytes per lane, turns the 8 x 8 blocks
 // in registers (v_perm), so no LDS is on the way, and multiplies by u or v, whose fp32
 // values enter as two bf16 terms (their sum has 16 bits, so the gradients' only rounding to
@@ -15,83 +15,6 @@
 
 namespace moe {
 namespace {
-
-constexpr int kSortThreads = 1024;
-constexpr int kSortWaves = kSortThreads / 64;
-
-// order: the tokens with an adapter, by adapter, ascending inside one; seg [S + 1]: where each
-// adapter's tokens begin.
-__global__ __launch_bounds__(kSortThreads) void order_kernel(PoolView P, int T, int32_t *order, int32_t *seg) {
-  extern __shared__ int hist[];  // [waves][S + 1] | start [S + 1]
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int n = P.S + 1;
-  int *start = hist + kSortWaves * n;
-  for (int i = tid; i < kSortWaves * n; i += kSortThreads) hist[i] = 0;
-  __syncthreads();
-  const int per = (T + kSortWaves - 1) / kSortWaves;
-  const int t0 = min(T, wave * per), t1 = min(T, t0 + per);
-  int rank;
-  for (int t = t0 + lane; t < t1; t += 64) {
-    const int s = adapter_of(P, t, rank);
-    if (s >= 0) atomicAdd(&hist[wave * n + s], 1);
-  }
-  __syncthreads();
-  for (int s = tid; s < n; s += kSortThreads) {
-    int run = 0;
-    for (int w = 0; w < kSortWaves; ++w) {
-      const int c = hist[w * n + s];
-      hist[w * n + s] = run;
-      run += c;
-    }
-    start[s] = run;
-  }
-  __syncthreads();
-  if (wave == 0) {  // exclusive scan over the adapters
-    const int each = (n + 63) / 64;
-    int local = 0;
-    for (int q = 0; q < each; ++q) local += lane * each + q < n ? start[lane * each + q] : 0;
-    int incl = local;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int o = __shfl_up(incl, off);
-      if (lane >= off) incl += o;
-    }
-    int run = incl - local;
-    for (int q = 0; q < each; ++q) {
-      const int s = lane * each + q;
-      if (s < n) {
-        const int c = start[s];
-        start[s] = run;
-        seg[s] = run;
-        run += c;
-      }
-    }
-  }
-  __syncthreads();
-  int *mine = hist + wave * n;
-  int bits = 0;
-  while ((1 << bits) < P.S) ++bits;
-  const uint64_t lt = (1ull << lane) - 1;
-  for (int b = t0; b < t1; b += 64) {
-    const int t = b + lane;
-    const int s = t < t1 ? adapter_of(P, t, rank) : -1;
-    const bool on = s >= 0;
-    uint64_t peers = __ballot(on);
-    for (int q = 0; q < bits; ++q) {
-      const bool bit = on && ((s >> q) & 1);
-      const uint64_t m = __ballot(bit);
-      peers &= bit ? m : ~m;
-    }
-    int at = 0;
-    if (on) at = mine[s];
-    wave_lds_fence();
-    if (on) {
-      order[start[s] + at + __popcll(peers & lt)] = t;
-      if ((peers & lt) == 0ull) mine[s] = at + __popcll(peers);
-    }
-    wave_lds_fence();
-  }
-}
 
 MOE_DEV uint32_t perm(uint32_t hi, uint32_t lo, uint32_t sel) { return __builtin_amdgcn_perm(hi, lo, sel); }
 
@@ -104,14 +27,88 @@ MOE_DEV void split8(const float (&v)[8], u32x4_t &hi, u32x4_t &lo) {
   }
 }
 
-constexpr int kGradWaves = 4;
+constexpr int kGradWaves = 8;
 constexpr int kGradCols = 128;
 
 // One workgroup: 128 columns of x (dA) or dy (dB), one adapter, RT * 16 ranks, one part of
-// the adapter's tokens.
+// the adapter's tokens; its wavefronts take pieces of 32 tokens in turn, each with the next
+// piece's token numbers loaded ahead.
+template <int RT, bool FOR_A, bool CODES>
+MOE_DEV void adapter_grad_sum(const AdapterGradArgs &P, int c, int r0, int lo, int hi, f32x4_t (&acc)[8][RT]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane & 15, grp = lane >> 4;
+  const int R = P.pool.R, ld = FOR_A ? P.ldx : P.ldy;
+  const float *q = FOR_A ? P.u : P.v;
+  const uint16_t *src = FOR_A ? P.x : P.dy;
+  const int nb = (P.K + kCkptBlock - 1) / kCkptBlock;
+  int p0 = lo + wave * 32, next[8];
+  auto tokens = [&](int p) MOE_INLINE {  // (past the end: the first token, its values are cleared)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) next[i] = P.order[p + grp * 8 + i < hi ? p + grp * 8 + i : lo];
+  };
+  if (p0 < hi) tokens(p0);
+  for (; p0 < hi; p0 += kGradWaves * 32) {
+    int tok[8];
+    bool on[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      tok[i] = next[i];
+      on[i] = p0 + grp * 8 + i < hi;
+    }
+    u32x4_t d[8];
+    if constexpr (CODES && FOR_A) {
+      u32x2_t w[8];
+      uint32_t e[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        w[i] = *reinterpret_cast<const u32x2_t *>(P.codes + (size_t)tok[i] * P.K + c);
+        e[i] = P.exps[(size_t)tok[i] * nb + c / kCkptBlock];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) d[i] = ckpt_to_bf16(w[i], ckpt_scale(e[i]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) d[i] = *reinterpret_cast<const u32x4_t *>(src + (size_t)tok[i] * ld + c);
+    }
+    float f[RT][8];
+#pragma unroll
+    for (int k = 0; k < RT; ++k) {
+      const int r = min(r0 + k * 16 + row, R - 1);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[k][i] = q[(size_t)tok[i] * R + r];
+    }
+    tokens(p0 + kGradWaves * 32);
+    // tokens past the segment's end: zeros on both sides
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (!on[i]) {
+        d[i] = zero_u32x4();
+#pragma unroll
+        for (int k = 0; k < RT; ++k) f[k][i] = 0.f;
+      }
+    u32x4_t qh[RT], ql[RT];
+#pragma unroll
+    for (int k = 0; k < RT; ++k) split8(f[k], qh[k], ql[k]);
+    // column j of the lane's 8 x 8 block: its 8 tokens
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      u32x4_t col;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        col[t] = perm(d[2 * t + 1][j >> 1], d[2 * t][j >> 1], (j & 1) ? 0x07060302u : 0x05040100u);
+#pragma unroll
+      for (int k = 0; k < RT; ++k) {
+        acc[j][k] = FOR_A ? mfma_16x16x32(col, qh[k], acc[j][k]) : mfma_16x16x32(qh[k], col, acc[j][k]);
+        acc[j][k] = FOR_A ? mfma_16x16x32(col, ql[k], acc[j][k]) : mfma_16x16x32(ql[k], col, acc[j][k]);
+      }
+    }
+  }
+}
+
 template <int RT, bool CODES>
 __global__ __launch_bounds__(kGradWaves * 64) void adapter_grad_kernel(const AdapterGradArgs P) {
-  __shared__ __attribute__((aligned(16))) f32x4_t join[2][8 * RT][64];
+  // sums of up to four wavefronts at a time (two, of 64 ranks: LDS)
+  constexpr int kJoin = RT <= 2 ? 4 : 2;
+  __shared__ __attribute__((aligned(16))) f32x4_t join[kJoin][8 * RT][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int row = lane & 15, grp = lane >> 4;
   const int R = P.pool.R, chunks = (R + RT * 16 - 1) / (RT * 16);
@@ -123,83 +120,37 @@ __global__ __launch_bounds__(kGradWaves * 64) void adapter_grad_kernel(const Ada
   const int seg0 = P.seg[slot], len = P.seg[slot + 1] - seg0;
   const int each = ((len + P.parts - 1) / P.parts + 31) & ~31;
   const int lo = seg0 + min(len, (int)blockIdx.z * each), hi = seg0 + min(len, ((int)blockIdx.z + 1) * each);
-
   const int c = min(c0 + row * 8, cols - 8);
-  const float *q = for_a ? P.u : P.v;
-  const uint16_t *src = for_a ? P.x : P.dy;
-  const int ld = for_a ? P.ldx : P.ldy;
-  const int nb = (P.K + kCkptBlock - 1) / kCkptBlock;
-  const bool codes = CODES && for_a;
 
   f32x4_t acc[8][RT];
 #pragma unroll
   for (int j = 0; j < 8; ++j)
 #pragma unroll
     for (int i = 0; i < RT; ++i) acc[j][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
   if (r0 < rank) {
-    for (int p0 = lo + wave * 32; p0 < hi; p0 += kGradWaves * 32) {
-      int tok[8];
-      bool on[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int p = p0 + grp * 8 + i;
-        on[i] = p < hi;
-        tok[i] = P.order[on[i] ? p : lo];
-      }
-      u32x4_t d[8];
-      if (codes) {
-        u32x2_t w[8];
-        uint32_t e[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          w[i] = *reinterpret_cast<const u32x2_t *>(P.codes + (size_t)tok[i] * P.K + c);
-          e[i] = P.exps[(size_t)tok[i] * nb + c / kCkptBlock];
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = ckpt_to_bf16(w[i], ckpt_scale(e[i]));
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = *reinterpret_cast<const u32x4_t *>(src + (size_t)tok[i] * ld + c);
-      }
-      u32x4_t qh[RT], ql[RT];
-#pragma unroll
-      for (int k = 0; k < RT; ++k) {
-        const int r = min(r0 + k * 16 + row, R - 1);
-        float f[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = q[(size_t)tok[i] * R + r];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = on[i] ? f[i] : 0.f;
-        split8(f, qh[k], ql[k]);
-      }
-      // tokens past the segment's end: zeros on both sides
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (!on[i]) d[i] = zero_u32x4();
-      // column j of the lane's 8 x 8 block: its 8 tokens
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        u32x4_t col;
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-          col[t] = perm(d[2 * t + 1][j >> 1], d[2 * t][j >> 1], (j & 1) ? 0x07060302u : 0x05040100u);
-#pragma unroll
-        for (int k = 0; k < RT; ++k) {
-          if (for_a) {
-            acc[j][k] = mfma_16x16x32(col, qh[k], acc[j][k]);
-            acc[j][k] = mfma_16x16x32(col, ql[k], acc[j][k]);
-          } else {
-            acc[j][k] = mfma_16x16x32(qh[k], col, acc[j][k]);
-            acc[j][k] = mfma_16x16x32(ql[k], col, acc[j][k]);
-          }
-        }
-      }
-    }
+    if (for_a)
+      adapter_grad_sum<RT, true, CODES>(P, c, r0, lo, hi, acc);
+    else
+      adapter_grad_sum<RT, false, CODES>(P, c, r0, lo, hi, acc);
   }
-  // the wavefronts' sums meet in the first one
+  // the wavefronts' sums meet in the first one, kJoin of them at a time and then halving
 #pragma unroll
-  for (int half = kGradWaves / 2; half >= 1; half >>= 1) {
+  for (int from = kGradWaves - kJoin; from >= kJoin; from -= kJoin) {
+    __syncthreads();
+    if (wave >= from && wave < from + kJoin)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int k = 0; k < RT; ++k) join[wave - from][j * RT + k][lane] = acc[j][k];
+    __syncthreads();
+    if (wave < kJoin)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int k = 0; k < RT; ++k) acc[j][k] += join[wave][j * RT + k][lane];
+  }
+#pragma unroll
+  for (int half = kJoin / 2; half >= 1; half >>= 1) {
     __syncthreads();
     if (wave >= half && wave < 2 * half)
 #pragma unroll
@@ -299,12 +250,12 @@ int launch_grad(const AdapterGradArgs &a, int col_tiles, hipStream_t s) {
 size_t up(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // Parts an adapter's tokens are cut into, so that few adapters still fill the device: about
-// two workgroups per compute unit, at least 256 tokens' worth each (of all tokens), 16 parts
+// 256 workgroups, at least 256 tokens' worth each (of all tokens), 16 parts
 // at most.
 int grad_parts(int T, int K, int N, int S, int R) {
   const int rt = R <= 16 ? 1 : R <= 32 ? 2 : 4;
   const long long wgs = (long long)((K + 127) / 128 + (N + 127) / 128) * S * ((R + rt * 16 - 1) / (rt * 16));
-  long long p = (512 + wgs - 1) / wgs;
+  long long p = (256 + wgs - 1) / wgs;
   const long long most = (T + 255) / 256;
   if (p > most) p = most;
   return (int)(p < 1 ? 1 : p > 16 ? 16 : p);
@@ -355,11 +306,12 @@ int launch_project_backward(const ProjectBackwardArgs &a, hipStream_t s) {
     uint16_t *ub = reinterpret_cast<uint16_t *>(ws + l.ub);
     float *u = reinterpret_cast<float *>(ws + l.u);
     // u over B [S, N, R]: the reduction runs over dy's N columns
-    if (a.dx || a.da) {
-      const ShrinkArgs sh{a.dy, a.ldy, a.T, a.N, a.b, a.pool, ub, u};
-      const int st = launch_shrink_transposed(sh, s);
-      if (st != ST_OK) return st;
-    }
+    const bool grads = a.da || a.db;
+    const ShrinkArgs sh{a.dy, a.ldy, a.T, a.N, a.b, a.pool, ub, u,
+                        grads ? reinterpret_cast<int32_t *>(ws + l.order) : nullptr,
+                        grads ? reinterpret_cast<int32_t *>(ws + l.seg) : nullptr};
+    const int st = launch_shrink_transposed(sh, s);
+    if (st != ST_OK) return st;
   }
   if (a.dx) {
     ProjectArgs p{};
@@ -398,13 +350,8 @@ int launch_project_backward(const ProjectBackwardArgs &a, hipStream_t s) {
   g.part_b = reinterpret_cast<float *>(ws + l.part_b);
   g.parts = l.parts;
   g.tiles_a = a.da ? (a.K + kGradCols - 1) / kGradCols : 0;
-  const size_t lds = (size_t)(kSortWaves + 1) * (S + 1) * sizeof(int);
-  order_kernel<<<1, kSortThreads, lds, s>>>(a.pool, a.T, reinterpret_cast<int32_t *>(ws + l.order),
-                                            reinterpret_cast<int32_t *>(ws + l.seg));
-  int st = ok();
-  if (st != ST_OK) return st;
   const int col_tiles = g.tiles_a + (a.db ? (a.N + kGradCols - 1) / kGradCols : 0);
-  st = a.codes ? launch_grad<true>(g, col_tiles, s) : launch_grad<false>(g, col_tiles, s);
+  const int st = a.codes ? launch_grad<true>(g, col_tiles, s) : launch_grad<false>(g, col_tiles, s);
   if (st != ST_OK || g.parts == 1) return st;
   const size_t n = (a.da ? (size_t)S * R * a.K : 0) + (a.db ? (size_t)S * R * a.N : 0);
   const size_t blocks = (n / 4 + 255) / 256;
