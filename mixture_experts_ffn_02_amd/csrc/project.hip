@@ -27,13 +27,14 @@ namespace {
 // MFMA operands through LDS of its own.
 constexpr int kShrinkWaves = 8;
 
-template <int RT, bool TR, bool LONG>
-__global__ __launch_bounds__(kShrinkWaves * 64, LONG ? 3 : 2) void shrink_kernel(const ShrinkArgs P) {
+template <int RT, int MT, bool TR, bool LONG>
+__global__ __launch_bounds__(kShrinkWaves * 64, LONG && MT == 1 ? 3 : 2) void shrink_kernel(const ShrinkArgs P) {
   constexpr int RP = RT * 16 + 1;
   constexpr int G = LONG ? (RT <= 2 ? 2 : 1) : RT <= 2 ? 4 : 2;
-  constexpr int kStage = kShrinkWaves * (16 + RT * 16) * 64 * 2, kPart = kShrinkWaves * 16 * RP * 4;
+  constexpr int ROWS = 16 * MT, XI = 2 * MT;
+  constexpr int kStage = kShrinkWaves * (ROWS + RT * 16) * 64 * 2, kPart = kShrinkWaves * ROWS * RP * 4;
   __shared__ __attribute__((aligned(16))) unsigned char smem[kStage > kPart ? kStage : kPart];
-  __shared__ int s_slot[16];
+  __shared__ int s_slot[ROWS];
   float *part = reinterpret_cast<float *>(smem);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   if (TR && P.order) {  // the first workgroup orders the tokens
@@ -44,24 +45,24 @@ __global__ __launch_bounds__(kShrinkWaves * 64, LONG ? 3 : 2) void shrink_kernel
       return;
     }
   }
-  const int t0 = ((int)blockIdx.x - (TR && P.order ? 1 : 0)) * 16;
+  const int t0 = ((int)blockIdx.x - (TR && P.order ? 1 : 0)) * ROWS;
   const int row = lane & 15, grp = lane >> 4;
+  // lane r < ROWS: row r's adapter; rows whose adapter no earlier row has (bits of those lanes)
   int rank_row = 0;
-  const int t_row = t0 + row;
-  int slot_row = t_row < P.T ? adapter_of(P.pool, t_row, rank_row) : -1;
-  // rows whose adapter no earlier row of the tile has (bits of lanes 0..15)
+  const int t_row = t0 + lane;
+  const int slot_row = lane < ROWS && t_row < P.T ? adapter_of(P.pool, t_row, rank_row) : -1;
   bool first = slot_row >= 0;
 #pragma unroll
-  for (int i = 0; i < 15; ++i) {
+  for (int i = 0; i < ROWS - 1; ++i) {
     const int o = __builtin_amdgcn_readlane(slot_row, i);
-    if (i < row && o == slot_row) first = false;
+    if (i < lane && o == slot_row) first = false;
   }
-  uint32_t todo = (uint32_t)(__ballot(first) & 0xffffull);
-  if (tid < 16) s_slot[tid] = slot_row;
+  uint32_t todo = (uint32_t)__ballot(first);
+  if (tid < ROWS) s_slot[tid] = slot_row;
   const int R = P.pool.R;
   __syncthreads();
   if (blockIdx.y == 0) {  // rows without an adapter
-    for (int i = tid; i < 16 * R; i += kShrinkWaves * 64) {
+    for (int i = tid; i < ROWS * R; i += kShrinkWaves * 64) {
       const int r = i / R, t = t0 + r;
       if (t < P.T && s_slot[r] < 0) {
         P.out_bf16[(size_t)t * R + i % R] = 0;
@@ -70,24 +71,26 @@ __global__ __launch_bounds__(kShrinkWaves * 64, LONG ? 3 : 2) void shrink_kernel
     }
   }
   for (int skip = 0; skip < (int)blockIdx.y && todo; ++skip) todo &= todo - 1;
-  uint16_t *stage = reinterpret_cast<uint16_t *>(smem) + wave * (16 + RT * 16) * 64;
-  uint16_t *stage_m = stage + 16 * 64;
+  uint16_t *stage = reinterpret_cast<uint16_t *>(smem) + wave * (ROWS + RT * 16) * 64;
+  uint16_t *stage_m = stage + ROWS * 64;
   const int lr = lane >> 3, lc = lane & 7;  // this lane's row of eight, and 16-byte chunk
   const int st_off = lr * 64 + ((lc ^ lr) << 3);
   const int steps = (P.K + 63) / 64, per = (steps + kShrinkWaves - 1) / kShrinkWaves;
   const int s_begin = min(steps, wave * per), s_end = min(steps, s_begin + per);
-  const uint16_t *xr[2];
+  const uint16_t *xr[XI];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) xr[i] = P.x + (size_t)min(t0 + i * 8 + lr, P.T - 1) * P.ldx + lc * 8;
+  for (int i = 0; i < XI; ++i) xr[i] = P.x + (size_t)min(t0 + i * 8 + lr, P.T - 1) * P.ldx + lc * 8;
   while (todo) {
     const int lead = __ffs(todo) - 1, slot = __builtin_amdgcn_readlane(slot_row, lead);
     for (int skip = 0; skip < (int)gridDim.y && todo; ++skip) todo &= todo - 1;
     const int rank = __builtin_amdgcn_readlane(rank_row, lead);
     const float scale = P.pool.scaling[slot];
     for (int r0 = 0; r0 < rank; r0 += RT * 16) {
-      f32x4_t acc[RT];
+      f32x4_t acc[MT][RT];
 #pragma unroll
-      for (int i = 0; i < RT; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int h = 0; h < MT; ++h)
+#pragma unroll
+        for (int i = 0; i < RT; ++i) acc[h][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       // TR: a step's rows n, each 2 RT chunks of 8 ranks; else 16 RT rank rows of 8 chunks
       const uint16_t *mp[2 * RT];
       int m_n[2 * RT];
@@ -100,11 +103,11 @@ __global__ __launch_bounds__(kShrinkWaves * 64, LONG ? 3 : 2) void shrink_kernel
         else
           mp[i] = P.m + ((size_t)slot * R + min(r0 + i * 8 + lr, R - 1)) * P.K + lc * 8;
       }
-      u32x4_t xg[G][2], mg[G][2 * RT];
+      u32x4_t xg[G][XI], mg[G][2 * RT];
       auto load = [&](int g, int s) {  // zeros past the run or K
         const bool in = s < s_end && s * 64 + lc * 8 < P.K;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) xg[g][i] = in ? *reinterpret_cast<const u32x4_t *>(xr[i] + s * 64) : zero_u32x4();
+        for (int i = 0; i < XI; ++i) xg[g][i] = in ? *reinterpret_cast<const u32x4_t *>(xr[i] + s * 64) : zero_u32x4();
 #pragma unroll
         for (int i = 0; i < 2 * RT; ++i) {
           if constexpr (TR)
@@ -123,7 +126,7 @@ __global__ __launch_bounds__(kShrinkWaves * 64, LONG ? 3 : 2) void shrink_kernel
         for (int g = 0; g < G; ++g) {
           if (s0 + g >= s_end) break;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) *reinterpret_cast<u32x4_t *>(stage + i * 512 + st_off) = xg[g][i];
+          for (int i = 0; i < XI; ++i) *reinterpret_cast<u32x4_t *>(stage + i * 512 + st_off) = xg[g][i];
 #pragma unroll
           for (int i = 0; i < 2 * RT; ++i)
             *reinterpret_cast<u32x4_t *>(stage_m + i * 512 + (TR ? lane * 8 : st_off)) = mg[g][i];
@@ -132,7 +135,9 @@ __global__ __launch_bounds__(kShrinkWaves * 64, LONG ? 3 : 2) void shrink_kernel
 #pragma unroll
           for (int kk = 0; kk < 2; ++kk) {
             const int off = row * 64 + (((kk * 4 + grp) ^ (row & 7)) << 3);
-            const u32x4_t xf = *reinterpret_cast<const u32x4_t *>(stage + off);
+            u32x4_t xf[MT];
+#pragma unroll
+            for (int h = 0; h < MT; ++h) xf[h] = *reinterpret_cast<const u32x4_t *>(stage + h * 16 * 64 + off);
 #pragma unroll
             for (int i = 0; i < RT; ++i) {
               u32x4_t mf;
@@ -143,7 +148,8 @@ __global__ __launch_bounds__(kShrinkWaves * 64, LONG ? 3 : 2) void shrink_kernel
               } else {
                 mf = *reinterpret_cast<const u32x4_t *>(stage_m + i * 16 * 64 + off);
               }
-              acc[i] = mfma_16x16x32(xf, mf, acc[i]);
+#pragma unroll
+              for (int h = 0; h < MT; ++h) acc[h][i] = mfma_16x16x32(xf[h], mf, acc[h][i]);
             }
           }
           wave_lds_fence();
@@ -152,15 +158,17 @@ __global__ __launch_bounds__(kShrinkWaves * 64, LONG ? 3 : 2) void shrink_kernel
       // join the wavefronts' sums (in their order)
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < RT; ++i)
+      for (int h = 0; h < MT; ++h)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) part[(wave * 16 + grp * 4 + q) * RP + i * 16 + row] = acc[i][q];
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) part[(wave * ROWS + h * 16 + grp * 4 + q) * RP + i * 16 + row] = acc[h][i][q];
       __syncthreads();
-      for (int c = tid; c < 16 * RT * 16; c += kShrinkWaves * 64) {
+      for (int c = tid; c < ROWS * RT * 16; c += kShrinkWaves * 64) {
         const int tr = c / (RT * 16), rc = c % (RT * 16), t = t0 + tr, r = r0 + rc;
         float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < kShrinkWaves; ++w) v += part[(w * 16 + tr) * RP + rc];
+        for (int w = 0; w < kShrinkWaves; ++w) v += part[(w * ROWS + tr) * RP + rc];
         if (s_slot[tr] != slot || r >= R) continue;
         if (r >= rank) v = 0.f;
         P.out_bf16[(size_t)t * R + r] = (uint16_t)f32_to_bf16(scale * v);
@@ -170,7 +178,7 @@ __global__ __launch_bounds__(kShrinkWaves * 64, LONG ? 3 : 2) void shrink_kernel
     // ranks past the last chunk that the loop above wrote
     const int done = (rank + RT * 16 - 1) / (RT * 16) * (RT * 16);
     if (done < R) {
-      for (int c = tid; c < 16 * (R - done); c += kShrinkWaves * 64) {
+      for (int c = tid; c < ROWS * (R - done); c += kShrinkWaves * 64) {
         const int tr = c / (R - done), t = t0 + tr, r = done + c % (R - done);
         if (s_slot[tr] != slot) continue;
         P.out_bf16[(size_t)t * R + r] = 0;
@@ -672,24 +680,26 @@ int ok() { return hipGetLastError() == hipSuccess ? ST_OK : ST_HIP; }
 
 constexpr int kFewTokens = 256;
 
-template <bool TR, bool LONG>
+template <int MT, bool TR, bool LONG>
 int launch_shrink_ranks(const ShrinkArgs &a, hipStream_t s) {
-  const dim3 grid((a.T + 15) / 16 + (TR && a.order ? 1 : 0), LONG ? 1 : 16);
+  const dim3 grid((a.T + 16 * MT - 1) / (16 * MT) + (TR && a.order ? 1 : 0), LONG ? 1 : 16);
   if (a.pool.R <= 16)
-    shrink_kernel<1, TR, LONG><<<grid, kShrinkWaves * 64, 0, s>>>(a);
+    shrink_kernel<1, MT, TR, LONG><<<grid, kShrinkWaves * 64, 0, s>>>(a);
   else if (a.pool.R <= 32)
-    shrink_kernel<2, TR, LONG><<<grid, kShrinkWaves * 64, 0, s>>>(a);
+    shrink_kernel<2, MT, TR, LONG><<<grid, kShrinkWaves * 64, 0, s>>>(a);
   else
-    shrink_kernel<4, TR, LONG><<<grid, kShrinkWaves * 64, 0, s>>>(a);
+    shrink_kernel<4, MT, TR, LONG><<<grid, kShrinkWaves * 64, 0, s>>>(a);
   return ok();
 }
 
-// A decode-sized batch takes a workgroup per (tile, adapter): up to 16 adapters meet in a
-// tile of 16 requests.  In longer batches a tile's few adapters follow each other, and two
-// workgroups share a compute unit.
+// A decode-sized batch takes a workgroup per (tile of 16, adapter): up to 16 adapters meet
+// in 16 requests.  In longer batches a tile's few adapters follow each other, and tiles of 32
+// tokens halve the reads of the adapters (4096 x 4096, rank 32, over B: 17.5 us in tiles of
+// 16, 12.6 of 32; the same 19 us either way where x comes from HBM).  Two steps in flight
+// there: four spill (18 us).
 template <bool TR>
 int launch_shrink(const ShrinkArgs &a, hipStream_t s) {
-  return a.T <= 1024 ? launch_shrink_ranks<TR, false>(a, s) : launch_shrink_ranks<TR, true>(a, s);
+  return a.T <= 1024 ? launch_shrink_ranks<1, TR, false>(a, s) : launch_shrink_ranks<2, TR, true>(a, s);
 }
 
 template <int FM, int FN, int W, int G>

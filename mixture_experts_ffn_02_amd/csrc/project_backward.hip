@@ -250,12 +250,12 @@ int launch_grad(const AdapterGradArgs &a, int col_tiles, hipStream_t s) {
 size_t up(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // Parts an adapter's tokens are cut into, so that few adapters still fill the device: about
-// 256 workgroups, at least 256 tokens' worth each (of all tokens), 16 parts
+// 192 workgroups, at least 256 tokens' worth each (of all tokens), 16 parts
 // at most.
 int grad_parts(int T, int K, int N, int S, int R) {
   const int rt = R <= 16 ? 1 : R <= 32 ? 2 : 4;
   const long long wgs = (long long)((K + 127) / 128 + (N + 127) / 128) * S * ((R + rt * 16 - 1) / (rt * 16));
-  long long p = (256 + wgs - 1) / wgs;
+  long long p = (192 + wgs - 1) / wgs;
   const long long most = (T + 255) / 256;
   if (p > most) p = most;
   return (int)(p < 1 ? 1 : p > 16 ? 16 : p);

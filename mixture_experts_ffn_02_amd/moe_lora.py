@@ -179,6 +179,14 @@ def _checked(name: str, t: torch.Tensor, dtype, numel: int) -> int:
     return t.data_ptr()
 
 
+def _workspace(ws: Optional[torch.Tensor]):
+    if ws is None:
+        return None, 0
+    if not ws.is_contiguous():
+        raise ValueError("ws: a contiguous tensor is needed")
+    return ws.data_ptr(), ws.nbytes
+
+
 def _call(fn: str, dev, stream, *args) -> None:
     """The library call with the tensors' device current (its kernels launch there), on the
     given stream or that device's current one."""
@@ -235,7 +243,7 @@ def moe_lora_route_scored(d: Dims, scoring: Scoring, logits, topk_ids, topk_weig
           ctypes.byref(d), ctypes.byref(sc), _checked("logits", logits, logits.dtype, T * E),
           _checked("topk_ids", topk_ids, i32, R), _checked("topk_weights", topk_weights, torch.float32, R),
           _checked("expert_offsets", expert_offsets, i32, E + 1), _checked("e2p", e2p, i32, R),
-          _checked("p2e", p2e, i32, R), _ptr(ws), ws.numel() * ws.element_size() if ws is not None else 0)
+          _checked("p2e", p2e, i32, R), *_workspace(ws))
 
 
 def moe_lora_route_scored_backward(d: Dims, scoring: Scoring, logits, topk_ids, d_weights, d_logits,
@@ -289,51 +297,62 @@ def moe_lora_finalize_backward(d: Dims, d_out, topk_weights, e2p, d_y_perm, d_we
           _checked("d_weights", d_weights, torch.float32, R))
 
 
-@dataclass
+@dataclass(frozen=True)
 class AdapterPool:
     """Resident adapters of a projection (device tensors): a [S, R, in] and b [S, out, R] bf16,
     rank [S] int32 and scaling [S] fp32; token_slot [T] int32 names each token's adapter
-    (outside [0, S): none)."""
+    (outside [0, S): none).
+
+    Checked when it is made and then fixed (the tensors' contents may change; with_slots gives
+    the same adapters for another batch).
+    """
 
     token_slot: torch.Tensor
     rank: torch.Tensor
     scaling: torch.Tensor
     a: torch.Tensor
     b: torch.Tensor
+    _c: _lib.Pool = field(init=False, repr=False, compare=False)
+    _shape: tuple = field(init=False, repr=False, compare=False)
 
-    def to_c(self, T: int, K: int, N: int) -> _lib.Pool:
+    def __post_init__(self):
         if self.a.dim() != 3 or self.b.dim() != 3:
             raise ValueError("a is [S, R, in] and b [S, out, R]")
-        S, R = self.a.shape[0], self.a.shape[1]
+        (S, R, K), N, T = self.a.shape, self.b.shape[1], self.token_slot.numel()
         bf16 = torch.bfloat16
-        return _lib.Pool(S, R, _checked("token_slot", self.token_slot, torch.int32, T),
-                         _checked("rank", self.rank, torch.int32, S),
-                         _checked("scaling", self.scaling, torch.float32, S),
-                         _checked("a", self.a, bf16, S * R * K), _checked("b", self.b, bf16, S * N * R))
+        object.__setattr__(self, "_c", _lib.Pool(
+            S, R, _checked("token_slot", self.token_slot, torch.int32, T),
+            _checked("rank", self.rank, torch.int32, S), _checked("scaling", self.scaling, torch.float32, S),
+            _checked("a", self.a, bf16, S * R * K), _checked("b", self.b, bf16, S * N * R)))
+        object.__setattr__(self, "_shape", (T, K, N))
+
+    def with_slots(self, token_slot: torch.Tensor) -> "AdapterPool":
+        return AdapterPool(token_slot, self.rank, self.scaling, self.a, self.b)
+
+    def to_c(self, T: int, K: int, N: int) -> _lib.Pool:
+        if self._shape != (T, K, N):
+            raise ValueError(f"the pool is for {self._shape[0]} tokens and a projection of {self._shape[1]} to "
+                             f"{self._shape[2]}, the call for {T}, {K} and {N}")
+        return self._c
 
 
-def _matrix(name: str, t: torch.Tensor, cols: int) -> int:
-    """Pointer of a bf16 matrix [*, cols] whose rows may lie apart (unit stride along them)."""
+def _matrix(name: str, t: torch.Tensor, rows: int, cols: int):
+    """Pointer and row pitch of a bf16 matrix [rows, cols] whose rows may lie apart."""
     if t.dtype is not torch.bfloat16 and t.dtype not in (torch.int16, torch.uint16):
         raise ValueError(f"{name}: torch.bfloat16 expected, got {t.dtype}")
-    if t.dim() != 2 or t.shape[1] != cols:
-        raise ValueError(f"{name}: [T, {cols}] expected, got shape {tuple(t.shape)}")
-    if t.shape[0] > 0 and (t.stride(1) != 1 or (t.shape[0] > 1 and t.stride(0) < cols)):
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name}: [{rows}, {cols}] expected, got shape {tuple(t.shape)}")
+    if rows == 0:
+        return t.data_ptr(), cols
+    pitch, unit = t.stride()
+    if unit != 1 or (rows > 1 and pitch < cols):
         raise ValueError(f"{name}: rows must have unit stride and not overlap")
-    return t.data_ptr()
-
-
-def _pitch(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
-def _proj_dims(T: int, K: int, N: int, x=None, y=None) -> _lib.ProjDims:
-    return _lib.ProjDims(T, K, N, K if x is None else _pitch(x), N if y is None else _pitch(y))
+    return t.data_ptr(), pitch if rows > 1 else cols
 
 
 def moe_lora_project_workspace_size(T: int, K: int, N: int, pool: AdapterPool) -> int:
-    p = pool.to_c(T, K, N)
-    return int(load().moe_lora_project_workspace_size(ctypes.byref(_proj_dims(T, K, N)), ctypes.byref(p)))
+    return int(load().moe_lora_project_workspace_size(ctypes.byref(_lib.ProjDims(T, K, N, K, N)),
+                                                      ctypes.byref(pool.to_c(T, K, N))))
 
 
 def moe_lora_project(x, w, pool: AdapterPool, y, ws, v=None, stream=None) -> None:
@@ -342,18 +361,17 @@ def moe_lora_project(x, w, pool: AdapterPool, y, ws, v=None, stream=None) -> Non
     T, K = _rows_cols("x", x)
     N = w.shape[0]
     p = pool.to_c(T, K, N)
-    if y.shape[0] != T:
-        raise ValueError(f"y: {T} rows expected, got {y.shape[0]}")
+    px, ldx = _matrix("x", x, T, K)
+    py, ldy = _matrix("y", y, T, N)
     _call("moe_lora_project", _on(x, w, y, ws, v, pool.token_slot, pool.rank, pool.scaling, pool.a, pool.b), stream,
-          ctypes.byref(_proj_dims(T, K, N, x, y)), _matrix("x", x, K), _checked("w", w, torch.bfloat16, N * K),
-          ctypes.byref(p), _matrix("y", y, N),
-          None if v is None else _checked("v", v, torch.float32, T * pool.a.shape[1]),
-          _ptr(ws), ws.numel() * ws.element_size() if ws is not None else 0)
+          ctypes.byref(_lib.ProjDims(T, K, N, ldx, ldy)), px, _checked("w", w, torch.bfloat16, N * K),
+          ctypes.byref(p), py, None if v is None else _checked("v", v, torch.float32, T * p.max_rank),
+          *_workspace(ws))
 
 
 def moe_lora_project_backward_workspace_size(T: int, K: int, N: int, pool: AdapterPool) -> int:
-    p = pool.to_c(T, K, N)
-    return int(load().moe_lora_project_backward_workspace_size(ctypes.byref(_proj_dims(T, K, N)), ctypes.byref(p)))
+    return int(load().moe_lora_project_backward_workspace_size(ctypes.byref(_lib.ProjDims(T, K, N, K, N)),
+                                                               ctypes.byref(pool.to_c(T, K, N))))
 
 
 def moe_lora_project_backward(dy, w, pool: AdapterPool, v, ws, x=None, x_codes=None, x_exps=None, dx=None, da=None,
@@ -362,22 +380,22 @@ def moe_lora_project_backward(dy, w, pool: AdapterPool, v, ws, x=None, x_codes=N
     wanted).  The input is x in bf16 or its checkpoint (x_codes, x_exps); v the forward's."""
     T, N = _rows_cols("dy", dy)
     K = w.shape[1]
-    S, R = pool.a.shape[0], pool.a.shape[1]
     p = pool.to_c(T, K, N)
+    S, R = p.num_slots, p.max_rank
     bf16, u8 = torch.bfloat16, torch.uint8
-    if x is not None and x.shape[0] != T:
-        raise ValueError(f"x: {T} rows expected, got {x.shape[0]}")
+    px, ldx = (None, K) if x is None else _matrix("x", x, T, K)
+    pdy, ldy = _matrix("dy", dy, T, N)
     _call("moe_lora_project_backward",
           _on(dy, w, v, ws, x, x_codes, x_exps, dx, da, db, pool.token_slot, pool.rank, pool.scaling, pool.a, pool.b),
-          stream, ctypes.byref(_proj_dims(T, K, N, x, dy)), None if x is None else _matrix("x", x, K),
+          stream, ctypes.byref(_lib.ProjDims(T, K, N, ldx, ldy)), px,
           None if x_codes is None else _checked("x_codes", x_codes, u8, T * K),
           None if x_exps is None else _checked("x_exps", x_exps, u8, T * ((K + 31) // 32)),
           _checked("w", w, bf16, N * K), ctypes.byref(p),
-          None if v is None else _checked("v", v, torch.float32, T * R), _matrix("dy", dy, N),
+          None if v is None else _checked("v", v, torch.float32, T * R), pdy,
           None if dx is None else _checked("dx", dx, bf16, T * K),
           None if da is None else _checked("da", da, bf16, S * R * K),
           None if db is None else _checked("db", db, bf16, S * N * R),
-          _ptr(ws), ws.numel() * ws.element_size() if ws is not None else 0)
+          *_workspace(ws))
 
 
 @dataclass

@@ -384,6 +384,10 @@ def test_binding_checks_shapes_types_and_strides():
         call(c.x, c.w[:, :56], c.pool, y, ws)
     with pytest.raises(ValueError, match="y"):
         call(c.x, c.w, c.pool, y[:11], ws)
+    with pytest.raises(ValueError, match="the pool is for"):
+        call(c.x[:11], c.w, c.pool, y[:11], ws)
+    with pytest.raises(ValueError, match="ws"):
+        call(c.x, c.w, c.pool, y, torch.empty((1 << 16, 2), dtype=torch.uint8, device=dev())[:, 0])
     with pytest.raises(ValueError, match="x:"):
         call(c.x.float(), c.w, c.pool, y, ws)
     with pytest.raises(ValueError, match="unit stride"):

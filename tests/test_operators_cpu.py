@@ -82,6 +82,27 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes():
         ml._checked("x", t.t(), torch.float32, 32)
 
 
+def test_pool_descriptor_refusals():
+    i32, bf16 = torch.int32, torch.bfloat16
+    good = dict(token_slot=torch.zeros(5, dtype=i32), rank=torch.ones(2, dtype=i32), scaling=torch.ones(2),
+                a=torch.zeros((2, 8, 16), dtype=bf16), b=torch.zeros((2, 24, 8), dtype=bf16))
+    pool = ml.AdapterPool(**good)
+    assert pool.to_c(5, 16, 24).max_rank == 8
+    assert pool.with_slots(torch.zeros(7, dtype=i32)).to_c(7, 16, 24).num_slots == 2
+    for bad in ((6, 16, 24), (5, 8, 24), (5, 16, 16)):
+        with pytest.raises(ValueError, match="the pool is for"):
+            pool.to_c(*bad)
+    for name, t in (("token_slot", torch.zeros(5)), ("rank", torch.ones(3, dtype=i32)), ("scaling", torch.ones(2).double()),
+                    ("a", torch.zeros((2, 8, 16))), ("b", torch.zeros((2, 24, 16), dtype=bf16)),
+                    ("a", torch.zeros((2, 16, 8), dtype=bf16).transpose(1, 2))):
+        with pytest.raises(ValueError, match=name):
+            ml.AdapterPool(**{**good, name: t})
+    with pytest.raises(ValueError):
+        ml.AdapterPool(**{**good, "a": torch.zeros((16, 16), dtype=bf16)})
+    with pytest.raises(AttributeError):
+        pool.rank = torch.ones(2, dtype=i32)
+
+
 # ---- the oracle's definitions
 def _logits(T, E, seed=0):
     return np.random.Generator(np.random.PCG64(seed)).standard_normal((T, E)) * 1.5
