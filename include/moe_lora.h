@@ -377,8 +377,9 @@ int moe_lora_checkpoint_unpack(int64_t rows, int32_t cols, const uint8_t *codes,
  *   d_weights[t, j] = sum_h d_out[t, h] * y_perm[e2p[t*k+j], h]               [T, k] fp32
  * (d_weights is what moe_lora_route_scored_backward takes.)  y_perm is given either in bf16
  * or as its checkpoint (y_codes and y_exps of T*k rows, y_perm NULL); giving both or neither
- * is MOE_LORA_ERR_INVALID_ARGUMENT.  A position outside [0, T*k) takes no part (its weight's
- * gradient is 0); rows that no position names are left as they were. */
+ * is MOE_LORA_ERR_INVALID_ARGUMENT.  The positions are distinct (as moe_lora_route's are).  One
+ * outside [0, T*k) takes no part (its weight's gradient is 0); rows that no position names
+ * are left as they were. */
 int moe_lora_finalize_backward(const moe_lora_dims *dims, const uint16_t *d_out, const uint16_t *y_perm,
                                const uint8_t *y_codes, const uint8_t *y_exps, const float *topk_weights,
                                const int32_t *expanded_to_permuted, uint16_t *d_y_perm,
@@ -394,9 +395,10 @@ int moe_lora_finalize_backward(const moe_lora_dims *dims, const uint16_t *d_out,
  *   x [T, in] rows ldx apart, w [out, in], y [T, out] rows ldy apart (columns between are
  *   left as they were), v [T, max_rank] fp32: A x unscaled, zero past a row's rank; written
  *   if not NULL (a backward pass takes it).
- * in and out: multiples of 8, in * out < 2^30; ldx and ldy multiples of 8, at most 2^22 (else
- * MOE_LORA_ERR_UNSUPPORTED).  T may be 0.  A token whose slot lies outside [0, num_slots), or
- * whose adapter has rank 0, gets the shared projection alone.
+ * in and out: multiples of 8, in * out < 2^30; ldx and ldy multiples of 8, at most 2^22; T at
+ * most 2^24, T * in and T * out at most 2^42 (else MOE_LORA_ERR_UNSUPPORTED).  T may be 0.  A token whose slot lies outside [0, num_slots), or
+ * whose adapter has rank 0, gets the shared projection alone.  A token or an adapter that
+ * holds infinities or NaN reaches the outputs of its own tokens only.
  * Workspace: moe_lora_project_workspace_size bytes, written before it is read; calls that
  * may overlap need one each. */
 #define MOE_LORA_MAX_POOL_SLOTS 512

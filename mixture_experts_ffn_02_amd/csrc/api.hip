@@ -449,6 +449,10 @@ int check_proj(const moe_lora_proj_dims *d, const moe_lora_pool *p, bool shape_o
   if (d->in_features % 8 != 0 || d->out_features % 8 != 0 || d->ldx % 8 != 0 || d->ldy % 8 != 0 ||
       d->ldx > (1 << 22) || d->ldy > (1 << 22) || (long long)d->in_features * d->out_features >= (1ll << 30))
     return MOE_LORA_ERR_UNSUPPORTED;
+  // (tile counts stay below 2^31)
+  if (d->num_tokens > (1 << 24) ||
+      (long long)d->num_tokens * (d->in_features > d->out_features ? d->in_features : d->out_features) > (1ll << 42))
+    return MOE_LORA_ERR_UNSUPPORTED;
   if (!p) return MOE_LORA_ERR_INVALID_ARGUMENT;
   if (p->num_slots < 0) return MOE_LORA_ERR_INVALID_ARGUMENT;
   if (p->num_slots > MOE_LORA_MAX_POOL_SLOTS) return MOE_LORA_ERR_UNSUPPORTED;

@@ -539,6 +539,7 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
   };
   issue(0, 0);
   exts = chunks * tile_adapters<BM, NT>(pool, t0, P.T, s_slot, s_list, s_bits);
+  if (tid == 0) s_bits[0] = 0u;  // from here on: whether an adapter holds what is not finite
   dma_wait_all();
   __syncthreads();
   issue(1, 1);
@@ -605,7 +606,6 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
   // adapter holds reaches them as 0 * inf or 0 * NaN, what is not finite in its rows is taken
   // out here and marks the adapter, whose outputs get it back at the end.  (Selecting
   // accumulators by row instead kept them out of the accumulation registers.)
-  if (tid == 0) s_bits[0] = 0u;
 #pragma unroll 1
   for (int e = 0; e < exts; ++e) {
     const int buf = (steps + e) & 1;

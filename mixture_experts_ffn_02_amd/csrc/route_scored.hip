@@ -141,10 +141,13 @@ MOE_DEV bool take_best(uint32_t (&hi)[N], uint32_t (&lo)[N], uint64_t lanes, uin
   return true;
 }
 
-// Whether fp32 keys a >= b (order keys of values) decide as the fp64 ones do: scores are off
-// by at most 2^-20 (exp, a sum of up to 512 terms and a division in fp32 around values of at
-// most 1: some 16 half steps of 2^-24), a key by a half step of itself more, a group's sum of
-// two by twice that.  Ties and what is not finite are not decided.
+// Whether fp32 keys a >= b (order keys of values) decide as the fp64 ones do.  In half steps of
+// 2^-24, around values of at most 1: a softmax sum takes 36 at most (32 terms in a lane and
+// four joins, 512 experts on 16 lanes), exp and the division some six, so a score is off by
+// less than 2^-18.5; with groups (64 lanes: 8 terms and six joins) by less than 2^-19.5, and a
+// sum of two keys by 2^-18.5.  Adding the bias takes a half step of the key.  A difference
+// above 2^-17 + 2^-20 of the keys is larger than two such errors.  Ties and what is not
+// finite are not decided.
 MOE_DEV bool decided(uint32_t a, uint32_t b) {
   const float x = key_f32(a), y = key_f32(b);
   return x - y > 0x1p-17f + 0x1p-20f * fmaxf(fabsf(x), fabsf(y)) && fabsf(x) < 1e30f;

@@ -424,7 +424,7 @@ class MoELoRALayer:
 
     def __init__(self, hidden: int, inter: int, num_experts: int, top_k: int,
                  w_gate_up: torch.Tensor, w_down: torch.Tensor,
-                 routing: int = ROUTING_RENORMALIZE, n_group: int = 1, topk_group: int = 1,
+                 routing=ROUTING_RENORMALIZE, n_group: int = 1, topk_group: int = 1,
                  routed_scaling_factor: float = 1.0, correction_bias: Optional[torch.Tensor] = None,
                  gather_on_load: bool = True, packed_weights=0, weights_prepacked=0,
                  w_gate_up_scale: Optional[torch.Tensor] = None, w_down_scale: Optional[torch.Tensor] = None,
@@ -453,6 +453,9 @@ class MoELoRALayer:
             w_down = w2p if w2p is not None else w_down
         self.packed_weights = to_pack | pre
         self.w_gate_up, self.w_down = w_gate_up, w_down
+        if isinstance(routing, Scoring) and (correction_bias is not None or
+                                             (n_group, topk_group, routed_scaling_factor) != (1, 1, 1.0)):
+            raise ValueError("a Scoring holds its own groups, scale and bias")
         self.routing = routing
         self.correction_bias = correction_bias
         self.grouped = None

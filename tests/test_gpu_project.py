@@ -137,7 +137,8 @@ SHAPES = [  # T, K, N, S, R, pad
     (1, 8, 8, 1, 8, 0), (1, 2048, 4096, 3, 16, 0), (5, 40, 24, 4, 24, 8), (16, 136, 712, 2, 128, 0),
     (17, 1000, 40, 20, 8, 64), (37, 264, 3080, 9, 32, 0), (64, 512, 256, 64, 16, 0), (200, 72, 136, 512, 8, 0),
     (256, 128, 64, 5, 64, 16), (257, 200, 72, 5, 24, 8), (300, 64, 1032, 7, 128, 0), (700, 328, 2056, 3, 40, 0),
-    (2049, 72, 2400, 4, 16, 0), (3100, 136, 4104, 6, 72, 0),
+    (2049, 72, 2400, 4, 16, 0), (3100, 136, 4104, 6, 72, 0), (300, 8, 8, 2, 8, 0), (1100, 64, 24, 3, 128, 0),
+    (513, 4104, 72, 2, 8, 0),
 ]
 
 

@@ -101,6 +101,21 @@ def test_masked_experts_and_masked_tokens(score, renorm):
     assert (run_route(t, 6, scoring(score, renorm))[1][5] == 0).all()
 
 
+def test_near_ties_fall_to_the_fp64_keys():
+    """Biases that put the sigmoid keys of neighbours 1e-9 apart, in both orders: far below fp32's
+    steps, so that the choice on fp32 keys cannot stand."""
+    T, E, k = 40, 64, 8
+    t, l = make_logits(T, E, "f32", 15)
+    t[1:] = t[0]
+    l = t.double().numpy()
+    p = 1 / (1 + np.exp(-l[0]))
+    want = np.linspace(0.9, 0.5, E // 2).repeat(2) + np.tile([0.0, 1e-9], E // 2)
+    bias = (want - p).astype(np.float32)  # fp32 rounds each key by up to 2^-25: order as it falls
+    check_route(t, l, k, scoring("sigmoid", True, bias), bias)
+    check_route(t, l, k, scoring("sigmoid", True, bias, n_group=8, topk_group=3, group_score=2), bias)
+    check_route(t, l, k, scoring("sigmoid", True, bias, n_group=8, topk_group=3, group_score=1), bias)
+
+
 def test_not_finite_logits_keep_the_ids_valid():
     t, _ = make_logits(66, 96, "f32", 4)
     t[0, 7] = float("nan")
@@ -199,14 +214,15 @@ def test_layer_runs_on_scored_routing():
     assert_layer_close(f64(out), g.oracle_layer()["out"], "scored grouped layer")
 
 
-def test_graph_replays_equal_eager():
-    t, _ = make_logits(300, 64, "f32", 11)
-    t2, _ = make_logits(300, 64, "f32", 12)
-    d, sc = ml.dims(300, 8, 8, 64, 4), scoring("softmax", False)
+@pytest.mark.parametrize("E,groups", [(64, 1), (512, 8)])  # the second: over 64 KiB of LDS
+def test_graph_replays_equal_eager(E, groups):
+    t, _ = make_logits(300, E, "f32", 11)
+    t2, _ = make_logits(300, E, "f32", 12)
+    d, sc = ml.dims(300, 8, 8, E, 4), scoring("softmax", False, n_group=groups, topk_group=(groups + 1) // 2, group_score=2)
     x = t.to(dev())
     i32 = dict(dtype=torch.int32, device=dev())
-    ids, off, e2p, p2e = (torch.empty(s, **i32) for s in ((300, 4), (65,), (1200,), (1200,)))
-    w, dl = torch.empty((300, 4), device=dev()), torch.empty((300, 64), device=dev())
+    ids, off, e2p, p2e = (torch.empty(s, **i32) for s in ((300, 4), (E + 1,), (1200,), (1200,)))
+    w, dl = torch.empty((300, 4), device=dev()), torch.empty((300, E), device=dev())
     ws = torch.empty((ml.moe_lora_route_scored_workspace_size(d, sc),), dtype=torch.uint8, device=dev())
 
     def step():

@@ -216,7 +216,8 @@ def _project(d, p, x=FAKE, w=FAKE, y=FAKE, v=None, ws=FAKE, ws_bytes=1 << 20):
     ((4, 64, 48, 56, 48), _lib.ERR_INVALID_ARGUMENT), ((4, 64, 48, 64, 40), _lib.ERR_INVALID_ARGUMENT),
     ((4, 60, 48, 64, 48), _lib.ERR_UNSUPPORTED), ((4, 64, 44, 64, 48), _lib.ERR_UNSUPPORTED),
     ((4, 64, 48, 68, 48), _lib.ERR_UNSUPPORTED), ((4, 64, 48, 64, 1 << 23), _lib.ERR_UNSUPPORTED),
-    ((4, 32768, 32768, 32768, 32768), _lib.ERR_UNSUPPORTED)])
+    ((4, 32768, 32768, 32768, 32768), _lib.ERR_UNSUPPORTED), (((1 << 24) + 1, 64, 48, 64, 48), _lib.ERR_UNSUPPORTED),
+    ((1 << 24, 64, 1 << 19, 64, 1 << 19), _lib.ERR_UNSUPPORTED)])
 def test_project_refuses_bad_sizes(dims, status):
     d = _lib.ProjDims(*dims)
     assert _project(d, _pool()) == status
