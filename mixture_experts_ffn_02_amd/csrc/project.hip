@@ -10,9 +10,9 @@
 // other adapters masked.  Rows keep token order; requests of a prompt are runs of tokens,
 // so a tile meets few adapters.
 //
-// Up to 256 tokens the weights' stream bounds the call: workgroups of 16 or 32 output
-// columns, K split over eight wavefronts, no LDS on the way in.  Above, tiles of up to
-// 256 x 256 from double-buffered LDS, filled by DMA loads.
+// Small calls (a few tokens, or few output tiles) are bound by the weights' stream and
+// latency: workgroups of 32 or 64 output columns, K split over eight wavefronts.  Larger ones
+// take tiles of up to 256 x 256 from double-buffered LDS, filled by DMA loads.
 #include "project.h"
 
 namespace moe {
@@ -678,8 +678,6 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
 
 int ok() { return hipGetLastError() == hipSuccess ? ST_OK : ST_HIP; }
 
-constexpr int kFewTokens = 256;
-
 template <int MT, bool TR, bool LONG>
 int launch_shrink_ranks(const ShrinkArgs &a, hipStream_t s) {
   const dim3 grid((a.T + 16 * MT - 1) / (16 * MT) + (TR && a.order ? 1 : 0), LONG ? 1 : 16);
@@ -709,10 +707,22 @@ int launch_few_tile(const ProjectArgs &a, hipStream_t s) {
   return ok();
 }
 
+// Tiles of 32 columns while they all run at once (one workgroup to a compute unit), of 64
+// beyond: a workgroup reads its tokens' rows of x whole, so wider tiles read x less often
+// (64 tokens, 2048 -> 4096, tiles of 16, 32 and 64 columns: 9.9, 8.7 and 11.5 us; 256 tokens:
+// 31.7, 16.4 and 12.6).
 int launch_few(const ProjectArgs &a, hipStream_t s) {
-  if (a.T <= 16) return launch_few_tile<1, 1, 8, 4>(a, s);
-  if (a.T <= 32) return launch_few_tile<2, 1, 8, 4>(a, s);
-  return launch_few_tile<4, 1, 8, 4>(a, s);
+  if (a.T <= 16) return launch_few_tile<1, 2, 8, 2>(a, s);
+  if (a.T <= 32) return launch_few_tile<2, 2, 8, 2>(a, s);
+  const long long at_32 = (long long)((a.T + 63) / 64) * ((a.N + 31) / 32);
+  return at_32 <= 256 ? launch_few_tile<4, 2, 8, 1>(a, s) : launch_few_tile<4, 4, 8, 1>(a, s);
+}
+
+// Whether the few-token kernel takes the call: while its widest tiles all run at once (512
+// tokens, 4096 -> 2048: 20.9 us against 32.9 in LDS tiles; 2048 -> 4096, two rounds of
+// workgroups: 23.6 against 18.9).
+bool takes_few(const ProjectArgs &a) {
+  return a.T <= 32 || (long long)((a.T + 63) / 64) * ((a.N + 63) / 64) <= 256;
 }
 
 template <int BM, int BN, int WM, int WN, bool NN>
@@ -743,7 +753,7 @@ int launch_project(const ProjectArgs &a, float *v, hipStream_t s) {
     const int st = launch_shrink<false>(sh, s);
     if (st != ST_OK) return st;
   }
-  if (a.T <= kFewTokens) return launch_few(a, s);
+  if (takes_few(a)) return launch_few(a, s);
   return launch_product<false>(a, s);
 }
 

@@ -138,7 +138,7 @@ SHAPES = [  # T, K, N, S, R, pad
     (17, 1000, 40, 20, 8, 64), (37, 264, 3080, 9, 32, 0), (64, 512, 256, 64, 16, 0), (200, 72, 136, 512, 8, 0),
     (256, 128, 64, 5, 64, 16), (257, 200, 72, 5, 24, 8), (300, 64, 1032, 7, 128, 0), (700, 328, 2056, 3, 40, 0),
     (2049, 72, 2400, 4, 16, 0), (3100, 136, 4104, 6, 72, 0), (300, 8, 8, 2, 8, 0), (1100, 64, 24, 3, 128, 0),
-    (513, 4104, 72, 2, 8, 0),
+    (513, 4104, 72, 2, 8, 0), (2500, 8, 1032, 2, 8, 0), (4200, 64, 776, 3, 128, 0), (600, 512, 1000, 3, 40, 8),
 ]
 
 
@@ -294,7 +294,7 @@ def test_requests_do_not_reach_each_other(T, mixed):
 def test_an_adapter_that_is_not_finite_shows_in_its_own_rows(T):
     """Infinities and NaN in two rows of one adapter's B: its tokens get NaN or infinities in those two
     outputs and their values elsewhere; nobody else's change."""
-    c = Case(T, 128, 1032, 3, 24, mixed=False, dirty=False)
+    c = Case(T, 128, 2056, 3, 24, mixed=False, dirty=False)
     c.slot[:] = runs(c.g, T, 3, 7)
     c.slot[T // 2:T // 2 + 5] = 1
     c.pool.token_slot.copy_(torch.from_numpy(c.slot))
@@ -308,7 +308,7 @@ def test_an_adapter_that_is_not_finite_shows_in_its_own_rows(T):
     y2 = c.forward()[0]
     mine = torch.from_numpy(c.slot == 1).to(dev())
     assert torch.equal(y[~mine], y2[~mine])
-    odd = torch.zeros(1032, dtype=torch.bool, device=dev())
+    odd = torch.zeros(2056, dtype=torch.bool, device=dev())
     odd[[5, 700]] = True
     assert not torch.isfinite(y2[mine][:, odd]).any()
     assert torch.equal(y[mine][:, ~odd], y2[mine][:, ~odd])
