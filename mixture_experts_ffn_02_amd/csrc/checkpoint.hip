@@ -7,7 +7,10 @@
 //
 // One thread holds 8 values (a 16-byte load), four neighbouring lanes a block; the maximum
 // joins over them with two DPP moves.  Bound by HBM: 2 bytes read and 1 + 1/32 written per
-// value (packing), the reverse for unpacking.
+// value (packing), the reverse for unpacking.  The codes, read a whole pass later, are stored
+// past the caches, and so are large unpacked rows (65536 x 2048 with the inputs in no cache:
+// packing 71.5 -> 70.1 us, unpacking 73.5 -> 70.9, 5.8 TB/s; with the same inputs again, which
+// then stay in the memory-side cache, 72.8 -> 60.9 and 74.8 -> 58.0).
 #include "checkpoint.h"
 #include "kernels.h"
 
@@ -90,7 +93,7 @@ struct CkptShape {
   int across, down;   // across * down <= kThreads
 };
 
-template <bool PACK>
+template <bool PACK, bool NT>
 __global__ __launch_bounds__(kThreads) void checkpoint_kernel(const CkptShape S, const uint16_t *__restrict__ src,
                                                               uint16_t *__restrict__ dst,
                                                               uint8_t *__restrict__ codes_out,
@@ -116,7 +119,7 @@ __global__ __launch_bounds__(kThreads) void checkpoint_kernel(const CkptShape S,
         uint32_t biased;
         const u32x2_t w = encode8(x[u], biased);
         if (row < S.rows) {
-          if (in) *reinterpret_cast<u32x2_t *>(codes_out + row * S.cols + c * 8) = w;
+          if (in) store_stream<NT>(reinterpret_cast<u32x2_t *>(codes_out + row * S.cols + c * 8), w);
           if ((c & 3) == 0) exps_out[row * S.blocks + (c >> 2)] = (uint8_t)biased;
         }
       }
@@ -137,7 +140,7 @@ __global__ __launch_bounds__(kThreads) void checkpoint_kernel(const CkptShape S,
       for (int u = 0; u < kRowsPerThread; ++u) {
         const long long row = row0 + u * S.down;
         if (in && row < S.rows)
-          *reinterpret_cast<u32x4_t *>(dst + row * S.cols + c * 8) = ckpt_to_bf16(w[u], ckpt_scale(e[u]));
+          store_stream<NT>(reinterpret_cast<u32x4_t *>(dst + row * S.cols + c * 8), ckpt_to_bf16(w[u], ckpt_scale(e[u])));
       }
     }
   }
@@ -162,14 +165,17 @@ unsigned grid_of(const CkptShape &s) {
 
 int launch_checkpoint_pack(long long rows, int cols, const uint16_t *x, uint8_t *codes, uint8_t *exps, hipStream_t s) {
   const CkptShape S = shape_of(rows, cols);
-  checkpoint_kernel<true><<<grid_of(S), kThreads, 0, s>>>(S, x, nullptr, codes, exps, nullptr, nullptr);
+  checkpoint_kernel<true, true><<<grid_of(S), kThreads, 0, s>>>(S, x, nullptr, codes, exps, nullptr, nullptr);
   return hipGetLastError() == hipSuccess ? ST_OK : ST_HIP;
 }
 
 int launch_checkpoint_unpack(long long rows, int cols, const uint8_t *codes, const uint8_t *exps, uint16_t *x,
                              hipStream_t s) {
   const CkptShape S = shape_of(rows, cols);
-  checkpoint_kernel<false><<<grid_of(S), kThreads, 0, s>>>(S, nullptr, x, nullptr, nullptr, codes, exps);
+  if ((size_t)rows * cols * 2 > kStreamBytes)
+    checkpoint_kernel<false, true><<<grid_of(S), kThreads, 0, s>>>(S, nullptr, x, nullptr, nullptr, codes, exps);
+  else
+    checkpoint_kernel<false, false><<<grid_of(S), kThreads, 0, s>>>(S, nullptr, x, nullptr, nullptr, codes, exps);
   return hipGetLastError() == hipSuccess ? ST_OK : ST_HIP;
 }
 

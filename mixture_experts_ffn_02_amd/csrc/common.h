@@ -36,6 +36,19 @@ MOE_DEV f32x4_t mfma_16x16x32(const u32x4_t &a, const u32x4_t &b, const f32x4_t 
                                                   __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
 }
 
+// Store past the caches where NT (outputs that the caches would not keep, or that nobody reads
+// soon), else an ordinary one.  A template argument: of two stores behind an ordinary branch
+// the compiler makes one, without the hint.
+template <bool NT, class T>
+MOE_DEV void store_stream(T *p, const T &v) {
+  if constexpr (NT)
+    __builtin_nontemporal_store(v, p);
+  else
+    *p = v;
+}
+// Outputs above half of the 256 MB that the memory-side cache holds are stored past it
+constexpr size_t kStreamBytes = 128u << 20;
+
 MOE_DEV int lane_id() { return __lane_id(); }
 
 MOE_DEV u32x4_t zero_u32x4() {

@@ -69,7 +69,8 @@ __global__ __launch_bounds__(kRowThreads) void finalize_kernel(const uint16_t *_
 // split the k choices, and a wavefront walks the row in 512-wide pieces with the piece of
 // d_out in registers for all of its choices (JN of them).  Products and sums in fp32, a
 // row's sum in a fixed order.  Bound by HBM: the routed rows are read once (2 bytes a
-// value, 1 + 1/32 from a checkpoint) and written once.
+// value, 1 + 1/32 from a checkpoint) and written once (8192 tokens, top-8, hidden 2048: 121 us
+// in bf16, 95 from a checkpoint, 4.7 TB/s; d_y stored past the caches: 121 and 102).
 template <int JN, bool CODES>
 __global__ __launch_bounds__(kRowThreads) void finalize_backward_kernel(const FinalizeBackwardArgs P) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
