@@ -47,6 +47,24 @@ __global__ __launch_bounds__(kShrinkWaves * 64, LONG && MT == 1 ? 3 : 2) void sh
   }
   const int t0 = ((int)blockIdx.x - (TR && P.order ? 1 : 0)) * ROWS;
   const int row = lane & 15, grp = lane >> 4;
+  const int lr = lane >> 3, lc = lane & 7;  // this lane's row of eight, and 16-byte chunk
+  const int st_off = lr * 64 + ((lc ^ lr) << 3);
+  const int steps = (P.K + 63) / 64, per = (steps + kShrinkWaves - 1) / kShrinkWaves;
+  const int s_begin = min(steps, wave * per), s_end = min(steps, s_begin + per);
+  const uint16_t *xr[XI];
+#pragma unroll
+  for (int i = 0; i < XI; ++i) xr[i] = P.x + (size_t)min(t0 + i * 8 + lr, P.T - 1) * P.ldx + lc * 8;
+  u32x4_t xg[G][XI];
+  auto load_x = [&](int g, int s) MOE_INLINE {  // zeros past the run or K
+    const bool in = s < s_end && s * 64 + lc * 8 < P.K;
+#pragma unroll
+    for (int i = 0; i < XI; ++i) xg[g][i] = in ? *reinterpret_cast<const u32x4_t *>(xr[i] + s * 64) : zero_u32x4();
+  };
+  // the first rows are on their way while the adapters are looked up (64 tokens, 2048 -> 4096:
+  // the whole call 17.5 us without, 17.3 so)
+#pragma unroll
+  for (int g = 0; g < G; ++g) load_x(g, s_begin + g);
+  bool fresh = true;  // those loads serve the first adapter
   // lane r < ROWS: row r's adapter; rows whose adapter no earlier row has (bits of those lanes)
   int rank_row = 0;
   const int t_row = t0 + lane;
@@ -73,13 +91,6 @@ __global__ __launch_bounds__(kShrinkWaves * 64, LONG && MT == 1 ? 3 : 2) void sh
   for (int skip = 0; skip < (int)blockIdx.y && todo; ++skip) todo &= todo - 1;
   uint16_t *stage = reinterpret_cast<uint16_t *>(smem) + wave * (ROWS + RT * 16) * 64;
   uint16_t *stage_m = stage + ROWS * 64;
-  const int lr = lane >> 3, lc = lane & 7;  // this lane's row of eight, and 16-byte chunk
-  const int st_off = lr * 64 + ((lc ^ lr) << 3);
-  const int steps = (P.K + 63) / 64, per = (steps + kShrinkWaves - 1) / kShrinkWaves;
-  const int s_begin = min(steps, wave * per), s_end = min(steps, s_begin + per);
-  const uint16_t *xr[XI];
-#pragma unroll
-  for (int i = 0; i < XI; ++i) xr[i] = P.x + (size_t)min(t0 + i * 8 + lr, P.T - 1) * P.ldx + lc * 8;
   while (todo) {
     const int lead = __ffs(todo) - 1, slot = __builtin_amdgcn_readlane(slot_row, lead);
     for (int skip = 0; skip < (int)gridDim.y && todo; ++skip) todo &= todo - 1;
@@ -103,11 +114,9 @@ __global__ __launch_bounds__(kShrinkWaves * 64, LONG && MT == 1 ? 3 : 2) void sh
         else
           mp[i] = P.m + ((size_t)slot * R + min(r0 + i * 8 + lr, R - 1)) * P.K + lc * 8;
       }
-      u32x4_t xg[G][XI], mg[G][2 * RT];
-      auto load = [&](int g, int s) {  // zeros past the run or K
+      u32x4_t mg[G][2 * RT];
+      auto load_m = [&](int g, int s) MOE_INLINE {
         const bool in = s < s_end && s * 64 + lc * 8 < P.K;
-#pragma unroll
-        for (int i = 0; i < XI; ++i) xg[g][i] = in ? *reinterpret_cast<const u32x4_t *>(xr[i] + s * 64) : zero_u32x4();
 #pragma unroll
         for (int i = 0; i < 2 * RT; ++i) {
           if constexpr (TR)
@@ -118,8 +127,13 @@ __global__ __launch_bounds__(kShrinkWaves * 64, LONG && MT == 1 ? 3 : 2) void sh
             mg[g][i] = in ? *reinterpret_cast<const u32x4_t *>(mp[i] + s * 64) : zero_u32x4();
         }
       };
+      if (!fresh) {
 #pragma unroll
-      for (int g = 0; g < G; ++g) load(g, s_begin + g);
+        for (int g = 0; g < G; ++g) load_x(g, s_begin + g);
+      }
+      fresh = false;
+#pragma unroll
+      for (int g = 0; g < G; ++g) load_m(g, s_begin + g);
       __syncthreads();  // the last round's sums have been read
       for (int s0 = s_begin; s0 < s_end; s0 += G) {
 #pragma unroll
@@ -130,7 +144,10 @@ __global__ __launch_bounds__(kShrinkWaves * 64, LONG && MT == 1 ? 3 : 2) void sh
 #pragma unroll
           for (int i = 0; i < 2 * RT; ++i)
             *reinterpret_cast<u32x4_t *>(stage_m + i * 512 + (TR ? lane * 8 : st_off)) = mg[g][i];
-          if (s0 + g + G < s_end) load(g, s0 + g + G);
+          if (s0 + g + G < s_end) {
+            load_x(g, s0 + g + G);
+            load_m(g, s0 + g + G);
+          }
           wave_lds_fence();
 #pragma unroll
           for (int kk = 0; kk < 2; ++kk) {
