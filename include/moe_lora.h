@@ -13,6 +13,10 @@
  *                      + down GEMM + down LoRA delta, unweighted, permuted rows
  *   moe_lora_finalize  routing-weighted top-k reduction back to token order
  *
+ * Around the layer: general routing scores and their gradient (moe_lora_route_scored),
+ * projections with pooled adapters and their gradients (moe_lora_project), rows kept in 8
+ * bits (moe_lora_checkpoint_pack), and the gradients of finalize.
+ *
  * Conventions (all calls):
  *   - Tensor pointers are DEVICE pointers unless marked [host].  bf16 tensors are
  *     passed as uint16_t bit patterns.  Every device pointer must be 16-byte aligned.
