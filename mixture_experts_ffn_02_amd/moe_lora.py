@@ -304,7 +304,8 @@ class AdapterPool:
     (outside [0, S): none).
 
     Checked when it is made and then fixed (the tensors' contents may change; with_slots gives
-    the same adapters for another batch).
+    the same adapters for another batch).  A tensor that was moved to other memory since
+    (resized, or given other data) is refused.
     """
 
     token_slot: torch.Tensor
@@ -314,17 +315,25 @@ class AdapterPool:
     b: torch.Tensor
     _c: _lib.Pool = field(init=False, repr=False, compare=False)
     _shape: tuple = field(init=False, repr=False, compare=False)
+    _at: tuple = field(init=False, repr=False, compare=False)
 
     def __post_init__(self):
         if self.a.dim() != 3 or self.b.dim() != 3:
             raise ValueError("a is [S, R, in] and b [S, out, R]")
         (S, R, K), N, T = self.a.shape, self.b.shape[1], self.token_slot.numel()
+        if self.b.shape != (S, N, R):
+            raise ValueError(f"b: [{S}, out, {R}] expected, got shape {tuple(self.b.shape)}")
         bf16 = torch.bfloat16
         object.__setattr__(self, "_c", _lib.Pool(
             S, R, _checked("token_slot", self.token_slot, torch.int32, T),
             _checked("rank", self.rank, torch.int32, S), _checked("scaling", self.scaling, torch.float32, S),
             _checked("a", self.a, bf16, S * R * K), _checked("b", self.b, bf16, S * N * R)))
         object.__setattr__(self, "_shape", (T, K, N))
+        object.__setattr__(self, "_at", self._addresses())
+
+    def _addresses(self):
+        return (self.token_slot.data_ptr(), self.rank.data_ptr(), self.scaling.data_ptr(), self.a.data_ptr(),
+                self.b.data_ptr())
 
     def with_slots(self, token_slot: torch.Tensor) -> "AdapterPool":
         return AdapterPool(token_slot, self.rank, self.scaling, self.a, self.b)
@@ -333,6 +342,8 @@ class AdapterPool:
         if self._shape != (T, K, N):
             raise ValueError(f"the pool is for {self._shape[0]} tokens and a projection of {self._shape[1]} to "
                              f"{self._shape[2]}, the call for {T}, {K} and {N}")
+        if self._at != self._addresses():
+            raise ValueError("a tensor of the pool was moved to other memory: make a new pool")
         return self._c
 
 

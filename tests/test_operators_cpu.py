@@ -103,6 +103,28 @@ def test_pool_descriptor_refusals():
         pool.rank = torch.ones(2, dtype=i32)
 
 
+def test_pool_whose_tensor_moved():
+    i32, bf16 = torch.int32, torch.bfloat16
+    for name in ("token_slot", "rank", "scaling", "a", "b"):
+        t = dict(token_slot=torch.zeros(5, dtype=i32), rank=torch.ones(2, dtype=i32), scaling=torch.ones(2),
+                 a=torch.zeros((2, 8, 16), dtype=bf16), b=torch.zeros((2, 24, 8), dtype=bf16))
+        pool = ml.AdapterPool(**t)
+        t[name].zero_()
+        pool.to_c(5, 16, 24)  # new contents
+        before = t[name].data
+        t[name].data = before.clone()
+        with pytest.raises(ValueError, match="moved"):
+            pool.to_c(5, 16, 24)
+
+
+def test_pool_with_another_order_of_ranks():
+    i32, bf16 = torch.int32, torch.bfloat16
+    with pytest.raises(ValueError, match="b:"):  # as many elements, other adapters
+        ml.AdapterPool(torch.zeros(5, dtype=i32), torch.ones(2, dtype=i32), torch.ones(2),
+                       torch.zeros((2, 8, 16), dtype=bf16), torch.zeros((4, 24, 4), dtype=bf16))
+
+
+
 # ---- the oracle's definitions
 def _logits(T, E, seed=0):
     return np.random.Generator(np.random.PCG64(seed)).standard_normal((T, E)) * 1.5
