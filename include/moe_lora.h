@@ -15,7 +15,8 @@
  *
  * Around the layer: general routing scores and their gradient (moe_lora_route_scored),
  * projections with pooled adapters and their gradients (moe_lora_project), rows kept in 8
- * bits (moe_lora_checkpoint_pack), and the gradients of finalize.
+ * bits (moe_lora_checkpoint_pack), and the gradients of finalize.  Their outputs overlap
+ * neither their inputs nor each other.
  *
  * Conventions (all calls):
  *   - Tensor pointers are DEVICE pointers unless marked [host].  bf16 tensors are
@@ -400,9 +401,10 @@ int moe_lora_finalize_backward(const moe_lora_dims *dims, const uint16_t *d_out,
  *   left as they were), v [T, max_rank] fp32: A x unscaled, zero past a row's rank; written
  *   if not NULL (a backward pass takes it).
  * in and out: multiples of 8, in * out < 2^30; ldx and ldy multiples of 8, at most 2^22; T at
- * most 2^24, T * in and T * out at most 2^42 (else MOE_LORA_ERR_UNSUPPORTED).  T may be 0.  A token whose slot lies outside [0, num_slots), or
- * whose adapter has rank 0, gets the shared projection alone.  A token or an adapter that
- * holds infinities or NaN reaches the outputs of its own tokens only.
+ * most 2^24, T * in and T * out at most 2^42 (else MOE_LORA_ERR_UNSUPPORTED).  T may be 0.
+ * A token whose slot lies outside [0, num_slots), or whose adapter has rank 0, gets the
+ * shared projection alone.  A token or an adapter that holds infinities or NaN reaches the
+ * outputs of its own tokens only (as infinities or NaN).
  * Workspace: moe_lora_project_workspace_size bytes, written before it is read; calls that
  * may overlap need one each. */
 #define MOE_LORA_MAX_POOL_SLOTS 512
@@ -438,7 +440,8 @@ int moe_lora_project(const moe_lora_proj_dims *dims, const uint16_t *x, const ui
  *   db[s] = scaling[s] * sum over them of dy[t] v[t]^T            [num_slots, out, max_rank]
  * all bf16, sums in fp32 (u enters dx rounded to bf16, da and db with 16 bits), every element
  * written: zeros for adapters without tokens and past an adapter's rank.  Repeated calls
- * give the same bits.  dx, da and db may each be NULL (not wanted; not all three).
+ * give the same bits.  Where the formula meets an infinity, da and db hold an infinity or
+ * NaN.  dx, da and db may each be NULL (not wanted; not all three).
  *   x: the forward's input in bf16 (rows dims->ldx apart), or its 8-bit checkpoint (x_codes,
  *   x_exps, x NULL); for da only.  w: for dx only.  v: the forward's v; for db only.
  * Giving both forms of x, or neither with da, is MOE_LORA_ERR_INVALID_ARGUMENT.

@@ -11,7 +11,7 @@
 // so a tile meets few adapters.
 //
 // Small calls (a few tokens, or few output tiles) are bound by the weights' stream and
-// latency: workgroups of 32 or 64 output columns, K split over eight wavefronts.  Larger ones
+// latency: workgroups of 16 to 64 output columns, K split over eight wavefronts.  Larger ones
 // take tiles of up to 256 x 256 from double-buffered LDS, filled by DMA loads.
 #include "project.h"
 
@@ -61,7 +61,7 @@ __global__ __launch_bounds__(kShrinkWaves * 64, LONG && MT == 1 ? 3 : 2) void sh
     for (int i = 0; i < XI; ++i) xg[g][i] = in ? *reinterpret_cast<const u32x4_t *>(xr[i] + s * 64) : zero_u32x4();
   };
   // the first rows are on their way while the adapters are looked up (64 tokens, 2048 -> 4096:
-  // the whole call 17.5 us without, 17.3 so)
+  // 0.3 us of the call)
 #pragma unroll
   for (int g = 0; g < G; ++g) load_x(g, s_begin + g);
   bool fresh = true;  // those loads serve the first adapter
@@ -212,7 +212,7 @@ __global__ __launch_bounds__(kShrinkWaves * 64, LONG && MT == 1 ? 3 : 2) void sh
 // products.  Eight neighbouring lanes load 128 contiguous bytes of a row, and each wavefront
 // turns its steps into MFMA operands through LDS of its own: loads in the operands' order
 // (neighbouring lanes in different rows) take one lane per cycle in the address path and
-// bounded the call (64 tokens, 2048 -> 4096: 13.6 us without adapters, 7.9 at 16 tokens).
+// bounded the call (64 tokens, 2048 -> 4096, in 64 x 32 tiles without adapters: 13.6 us, 9.8 so).
 template <int FM, int FN, int W, int G>
 __global__ __launch_bounds__(W * 64) void project_few_kernel(const ProjectArgs P) {
   constexpr int BM = FM * 16, BN = FN * 16, NT = W * 64;
@@ -724,15 +724,21 @@ int launch_few_tile(const ProjectArgs &a, hipStream_t s) {
   return ok();
 }
 
-// Tiles of 32 columns while they all run at once (one workgroup to a compute unit), of 64
-// beyond: a workgroup reads its tokens' rows of x whole, so wider tiles read x less often
-// (64 tokens, 2048 -> 4096, tiles of 16, 32 and 64 columns: 9.9, 8.7 and 11.5 us; 256 tokens:
-// 31.7, 16.4 and 12.6).
+// The smallest tiles that all run at once (one workgroup to a compute unit): more of the
+// device loads, and each workgroup less; wider tiles beyond, since a workgroup reads its
+// tokens' rows of x whole.  (Inputs in no cache, without adapters: 64 tokens, 2048 -> 4096 in
+// tiles of 64 x 32, 32 x 32 and 32 x 16: 10.4, 8.4 and 9.2 us; 64 tokens, 2048 -> 1024 in 64
+// x 32, 32 x 16 and 16 x 16: 8.0, 5.2 and 4.4; 128 tokens, 2048 -> 4096 in 64 x 32 and 32 x
+// 32: 10.5 and 11.1; 256 tokens, 2048 -> 4096 in 64 x 32 and 64 x 64: 16.4 and 12.6.)
 int launch_few(const ProjectArgs &a, hipStream_t s) {
+  auto fits = [&](int tokens, int cols) {
+    return (long long)((a.T + tokens - 1) / tokens) * ((a.N + cols - 1) / cols) <= 256;
+  };
+  if (fits(16, 16)) return launch_few_tile<1, 1, 8, 2>(a, s);
   if (a.T <= 16) return launch_few_tile<1, 2, 8, 2>(a, s);
-  if (a.T <= 32) return launch_few_tile<2, 2, 8, 2>(a, s);
-  const long long at_32 = (long long)((a.T + 63) / 64) * ((a.N + 31) / 32);
-  return at_32 <= 256 ? launch_few_tile<4, 2, 8, 1>(a, s) : launch_few_tile<4, 4, 8, 1>(a, s);
+  if (fits(32, 16)) return launch_few_tile<2, 1, 8, 2>(a, s);
+  if (a.T <= 32 || fits(32, 32)) return launch_few_tile<2, 2, 8, 1>(a, s);
+  return fits(64, 32) ? launch_few_tile<4, 2, 8, 1>(a, s) : launch_few_tile<4, 4, 8, 1>(a, s);
 }
 
 // Whether the few-token kernel takes the call: while its widest tiles all run at once (512
