@@ -56,6 +56,11 @@ MOE_DEV void dma16_if(int on, const void *base, uint32_t off, uint32_t lds) {
       : "v"(off), "s"(base), "s"(lds), "s"(on), "n"(LDS)
       : "memory", "scc");
 }
+// until at most N of the wavefront's loads are on their way (they land in order)
+template <int N>
+MOE_DEV void dma_wait() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
 MOE_DEV void dma_wait_all() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // f(integral_constant<D>) for D = BEGIN .. END - 1

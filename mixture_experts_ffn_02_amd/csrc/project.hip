@@ -6,8 +6,8 @@
 // tokens and one adapter per workgroup, K split over its wavefronts and joined in LDS.  The
 // rounding of s_a v to bf16 feeds the matrix cores and is the expert layer's own (its
 // error is 2^-9 of the delta, below the rounding of y).  The product appends the expand to
-// its K loop: one step per adapter among the tile's rows and 64 ranks, with the rows of the
-// other adapters masked.  Rows keep token order; requests of a prompt are runs of tokens,
+// its K loop: one step per 64 ranks of the adapters among the tile's rows, with the rows of
+// the other adapters masked.  Rows keep token order; requests of a prompt are runs of tokens,
 // so a tile meets few adapters.
 //
 // Small calls (a few tokens, or few output tiles) are bound by the weights' stream and
@@ -382,9 +382,10 @@ MOE_DEV void restore_odd(const ProjectArgs &P, int slot, int n, u32x4_t &v) {
   }
 }
 
-// One BM x BN tile per workgroup, 64-wide K steps double-buffered in LDS, both operands by
-// DMA loads one step ahead (rows of x and W past the matrix repeat its last row, chunks
-// past K read zeros).  The expand's steps follow in the same pipeline.
+// One BM x BN tile per workgroup, 64-wide K steps buffered in LDS, both operands by DMA
+// loads one step ahead (rows of x and W past the matrix repeat its last row, chunks
+// past K read zeros; small tiles three steps ahead).  The expand's steps follow in the same
+// pipeline.
 //   NN = 0: w [N, K], ext_b [S, N, R] (reduction contiguous)
 //   NN = 1: w [K, N], ext_b [S, R, N] (reduction by rows: operands read transposed from LDS)
 // LDS: rows of 64 bf16 in eight 16-byte chunks XOR-swizzled by the row (A, and B when
@@ -398,9 +399,11 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
   constexpr int A_IT = BM * 8 / NT, B_IT = BN * 8 / NT;
   constexpr int BCH = BN / 8;  // chunks per row of B (NN)
   constexpr int SWZ = BN / 16 < 8 ? BN / 16 - 1 : 7;  // its pairs' swizzle stays inside a row
-  __shared__ __attribute__((aligned(16))) uint16_t smem[2 * (BM + BN) * 64];
+  constexpr bool kRing = BM * BN <= 4096;
+  constexpr int NB = kRing ? 4 : 2;  // steps held in LDS
+  __shared__ __attribute__((aligned(16))) uint16_t smem[NB * (BM + BN) * 64];
   uint16_t(*As)[BM * 64] = reinterpret_cast<uint16_t(*)[BM * 64]>(smem);
-  uint16_t(*Bs)[BN * 64] = reinterpret_cast<uint16_t(*)[BN * 64]>(smem + 2 * BM * 64);
+  uint16_t(*Bs)[BN * 64] = reinterpret_cast<uint16_t(*)[BN * 64]>(smem + NB * BM * 64);
   __shared__ int s_slot[BM], s_list[BM];
   __shared__ uint32_t s_bits[16];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -448,50 +451,62 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
   }
   const uint16_t *a_base = P.x + (size_t)t0 * P.ldx;
   const uint16_t *b_base = NN ? P.w + n0 : P.w + (size_t)n0 * K;
-  const uint32_t a_lds[2] = {lds_byte(&As[0][0]) + wave * 1024, lds_byte(&As[1][0]) + wave * 1024};
-  const uint32_t b_lds[2] = {lds_byte(&Bs[0][0]) + wave * 1024, lds_byte(&Bs[1][0]) + wave * 1024};
+  auto a_lds = [&](int buf) MOE_INLINE { return lds_byte(&As[0][0]) + wave * 1024 + buf * (BM * 128); };
+  auto b_lds = [&](int buf) MOE_INLINE { return lds_byte(&Bs[0][0]) + wave * 1024 + buf * (BN * 128); };
 
   auto issue_full = [&](int buf, int k0) MOE_INLINE {
     const uint16_t *ab = a_base + k0;
     const uint16_t *bb = NN ? b_base + (size_t)k0 * N : b_base + k0;
 #pragma unroll
-    for (int i = 0; i < A_IT; ++i) dma16(ab, a_off[i], a_lds[buf] + i * NT * 16);
+    for (int i = 0; i < A_IT; ++i) dma16(ab, a_off[i], a_lds(buf) + i * NT * 16);
 #pragma unroll
-    for (int i = 0; i < B_IT; ++i) dma16(bb, b_off[i], b_lds[buf] + i * NT * 16);
+    for (int i = 0; i < B_IT; ++i) dma16(bb, b_off[i], b_lds(buf) + i * NT * 16);
   };
   auto issue_tail = [&](int buf, int k0) MOE_INLINE {  // chunks past K are zeros
     const char *ab = reinterpret_cast<const char *>(a_base + k0);
     const char *bb = reinterpret_cast<const char *>(NN ? b_base + (size_t)k0 * N : b_base + k0);
 #pragma unroll
     for (int i = 0; i < A_IT; ++i)
-      dma16(k0 + a_k(i) < K ? ab + a_off[i] : reinterpret_cast<const char *>(kZeroChunk), a_lds[buf] + i * NT * 16);
+      dma16(k0 + a_k(i) < K ? ab + a_off[i] : reinterpret_cast<const char *>(kZeroChunk), a_lds(buf) + i * NT * 16);
 #pragma unroll
     for (int i = 0; i < B_IT; ++i)
-      dma16(k0 + b_k(i) < K ? bb + b_off[i] : reinterpret_cast<const char *>(kZeroChunk), b_lds[buf] + i * NT * 16);
+      dma16(k0 + b_k(i) < K ? bb + b_off[i] : reinterpret_cast<const char *>(kZeroChunk), b_lds(buf) + i * NT * 16);
   };
-  // ranks [r0, r0 + 64) of one adapter
-  auto issue_ext = [&](int buf, int slot, int r0, int rank) MOE_INLINE {
+  // A step of the expand holds `per` adapters of up to 32 ranks side by side, or 64 ranks of
+  // one: ranks [r0, r0 + 64) of the adapters at [first, first + count) of the list.  (A step
+  // for each adapter: 8192 tokens of 8 mixed adapters of rank 16, 2048 -> 4096: 230 us, 179
+  // so; dx of 64 tokens of 32 adapters 61 us, 40 so.)
+  const int R = pool.R, per = R <= 32 ? 64 / R : 1;
+  // reduction index k of a step: its adapter (slot | rank << 16) and rank there; false: none
+  auto ext_at = [&](int first, int count, int r0, int k, int &entry, int &r) MOE_INLINE {
+    const int j = per > 1 ? k / R : 0;
+    r = r0 + k - j * R;
+    entry = s_list[first + min(j, count - 1)];
+    return j < count && r < list_rank(entry);
+  };
+  auto issue_ext = [&](int buf, int first, int count, int r0) MOE_INLINE {
     const char *z = reinterpret_cast<const char *>(kZeroChunk);
+    static_assert(NT % 64 == 0, "a thread's chunks of rows of 64 are at one reduction index");
+    int entry, r;
+    const bool live = ext_at(first, count, r0, a_k(0), entry, r);
 #pragma unroll
     for (int i = 0; i < A_IT; ++i) {
-      const int r = (i * NT + tid) >> 3;
-      const bool on = r0 + a_k(i) < rank && s_slot[r] == slot;
-      dma16(on ? reinterpret_cast<const char *>(P.ext_a + (size_t)(t0 + r) * pool.R + r0 + a_k(i)) : z,
-            a_lds[buf] + i * NT * 16);
+      const int t = (i * NT + tid) >> 3;
+      const bool on = live && s_slot[t] == list_slot(entry);
+      dma16(on ? reinterpret_cast<const char *>(P.ext_a + (size_t)(t0 + t) * R + r) : z, a_lds(buf) + i * NT * 16);
     }
 #pragma unroll
     for (int i = 0; i < B_IT; ++i) {
       const char *src = z;
       if constexpr (!NN) {
         const int n = n0 + ((i * NT + tid) >> 3);
-        if (r0 + b_k(i) < rank && n < N)
-          src = reinterpret_cast<const char *>(P.ext_b + ((size_t)slot * N + n) * pool.R + r0 + b_k(i));
+        if (live && n < N) src = reinterpret_cast<const char *>(P.ext_b + ((size_t)list_slot(entry) * N + n) * R + r);
       } else {
         const int q = i * NT + tid, c = (q % BCH) ^ ((((b_k(i) & 3) | ((b_k(i) >> 1) & 4)) & SWZ) << 1);
-        if (r0 + b_k(i) < rank && n0 + c * 8 < N)
-          src = reinterpret_cast<const char *>(P.ext_b + ((size_t)slot * pool.R + r0 + b_k(i)) * N + n0 + c * 8);
+        if (ext_at(first, count, r0, b_k(i), entry, r) && n0 + c * 8 < N)
+          src = reinterpret_cast<const char *>(P.ext_b + ((size_t)list_slot(entry) * R + r) * N + n0 + c * 8);
       }
-      dma16(src, b_lds[buf] + i * NT * 16);
+      dma16(src, b_lds(buf) + i * NT * 16);
     }
   };
 
@@ -535,13 +550,14 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
   // of the next step's first operands.  (DMA loads in one burst instead held the products
   // up: 8192 x 2048 -> 4096 in 137 us against 129, dx of 4096 x 4096 -> 2048 in 69 against 61.)
   const int steps = (K + 63) / 64, full = K / 64;
-  const int chunks = (pool.R + 63) / 64;  // 64-rank chunks per adapter
-  int exts = 0;                           // known once the adapters are listed
-  auto ext_of = [&](int e, int &slot, int &r0, int &rank) MOE_INLINE {
-    const int entry = __builtin_amdgcn_readfirstlane(s_list[e / chunks]);
-    slot = list_slot(entry);
-    r0 = (e % chunks) * 64;
-    rank = list_rank(entry);
+  const int chunks = (R + 63) / 64;  // steps of an adapter of more than 32 ranks
+  int adapters = 0, exts = 0;        // known once the adapters are listed
+  // the e-th step of the expand; left: its reduction's length (may be 0 or less)
+  auto ext_of = [&](int e, int &first, int &count, int &r0, int &left) MOE_INLINE {
+    first = per > 1 ? e * per : e / chunks;
+    count = min(per, adapters - first);
+    r0 = per > 1 ? 0 : (e - first * chunks) * 64;
+    left = per > 1 ? count * R : list_rank(__builtin_amdgcn_readfirstlane(s_list[first])) - r0;
   };
   auto issue = [&](int buf, int s) MOE_INLINE {
     if (s < full) {
@@ -549,18 +565,87 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
     } else if (s < steps) {
       issue_tail(buf, s * 64);
     } else if (s < steps + exts) {
-      int slot, r0, rank;
-      ext_of(s - steps, slot, r0, rank);
-      issue_ext(buf, slot, r0, rank);
+      int first, count, r0, left;
+      ext_of(s - steps, first, count, r0, left);
+      issue_ext(buf, first, count, r0);
     }
   };
   issue(0, 0);
-  exts = chunks * tile_adapters<BM, NT>(pool, t0, P.T, s_slot, s_list, s_bits);
+  adapters = tile_adapters<BM, NT>(pool, t0, P.T, s_slot, s_list, s_bits);
+  exts = per > 1 ? (adapters + per - 1) / per : chunks * adapters;
   if (tid == 0) s_bits[0] = 0u;  // from here on: whether an adapter holds what is not finite
+  // The expand.  Other requests' rows of the A operand are zeros; so that nothing that an
+  // adapter holds reaches them as 0 * inf or 0 * NaN, what is not finite in its rows is taken
+  // out here and marks the adapter, whose outputs get it back at the end.  (Selecting
+  // accumulators by row instead kept them out of the accumulation registers.)
+  auto clean = [&](int buf, int first, int count, int r0) MOE_INLINE {
+    bool odd = false;
+    int ranks = 64;  // of the chunk's adapter, from the chunk's first on
+    if constexpr (!NN) {
+      int entry, r;
+      ranks = ext_at(first, count, r0, b_k(0), entry, r) ? list_rank(entry) - r : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < B_IT; ++i) {
+      u32x4_t *p = reinterpret_cast<u32x4_t *>(&Bs[buf][(i * NT + tid) * 8]);
+      u32x4_t v = *p;
+      bool change = false;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const uint32_t half_mask = c & 1 ? 0xffff0000u : 0x0000ffffu;
+        // (NN = 0: ranks past the adapter's, whatever the pool holds there)
+        const bool past = !NN && c >= ranks;
+        const bool bad = (v[c >> 1] & half_mask & 0x7f807f80u) == (half_mask & 0x7f807f80u);
+        odd |= bad && !past;
+        change |= bad || past;
+        v[c >> 1] &= bad || past ? ~half_mask : 0xffffffffu;
+      }
+      if (change) *p = v;
+    }
+    if (odd) atomicOr(&s_bits[0], 1u);
+  };
+  u32x4_t af1[FM], bf1[FN];
+  // A small tile's steps are short beside the loads' latency: four of them in LDS, three on
+  // their way (dx without adapters, 64 tokens, 4096 -> 2048: 32.1 -> 24.4 us; 512: 33 -> 25).
+  if constexpr (kRing) {
+    constexpr int kLoads = A_IT + B_IT;  // of a wavefront for one step, whichever it is
+    const int total = steps + exts;
+    issue(1, 1);
+    issue(2, 2);
+#pragma unroll 1
+    for (int s = 0; s < total; ++s) {
+      if (s + 2 < total)
+        dma_wait<2 * kLoads>();
+      else
+        dma_wait_all();
+      __syncthreads();
+      issue((s + 3) & 3, s + 3);
+      const int buf = s & 3;
+      int left = 64;
+      if (s >= steps) {
+        int first, count, r0;
+        ext_of(s - steps, first, count, r0, left);
+        if (left > 0) {
+          clean(buf, first, count, r0);
+          __syncthreads();
+        }
+      }
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        if (kk * 32 >= left) break;
+#pragma unroll
+        for (int c = 0; c < kReads; ++c) read(buf, kk, c, af1, bf1);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j) acc[i][j] = mfma_16x16x32(bf1[j], af1[i], acc[i][j]);
+      }
+    }
+  } else {
   dma_wait_all();
   __syncthreads();
   issue(1, 1);
-  u32x4_t af0[FM], bf0[FN], af1[FM], bf1[FN];
+  u32x4_t af0[FM], bf0[FN];
 #pragma unroll
   for (int c = 0; c < kReads; ++c) read(0, 0, c, af0, bf0);
 
@@ -568,9 +653,9 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
   auto dma_one = [&](auto dc, int dbuf, const uint16_t *ab, const uint16_t *bb, int live) MOE_INLINE {
     constexpr int d = decltype(dc)::value;
     if constexpr (d < A_IT)
-      dma16_if<d * NT * 16>(live, ab, a_off[d], a_lds[dbuf]);
+      dma16_if<d * NT * 16>(live, ab, a_off[d], a_lds(dbuf));
     else
-      dma16_if<(d - A_IT) * NT * 16>(live, bb, b_off[d - A_IT], b_lds[dbuf]);
+      dma16_if<(d - A_IT) * NT * 16>(live, bb, b_off[d - A_IT], b_lds(dbuf));
   };
   // products of one half among the reads of (buf, kk); with dma, also among the DMA loads at
   // k0 into dbuf
@@ -619,36 +704,13 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
     if (s + 1 < steps) main_step(1, s + 1);
   }
 
-  // The expand.  Other requests' rows of the A operand are zeros; so that nothing that an
-  // adapter holds reaches them as 0 * inf or 0 * NaN, what is not finite in its rows is taken
-  // out here and marks the adapter, whose outputs get it back at the end.  (Selecting
-  // accumulators by row instead kept them out of the accumulation registers.)
 #pragma unroll 1
   for (int e = 0; e < exts; ++e) {
     const int buf = (steps + e) & 1;
-    int slot, r0, rank;
-    ext_of(e, slot, r0, rank);
-    const int left = rank - r0;
+    int first, count, r0, left;
+    ext_of(e, first, count, r0, left);
     if (left > 0) {
-      bool odd = false;
-#pragma unroll
-      for (int i = 0; i < B_IT; ++i) {
-        u32x4_t *p = reinterpret_cast<u32x4_t *>(&Bs[buf][(i * NT + tid) * 8]);
-        u32x4_t v = *p;
-        bool change = false;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const uint32_t half_mask = c & 1 ? 0xffff0000u : 0x0000ffffu;
-          // (NN = 0: ranks past the adapter's, whatever the pool holds there)
-          const bool past = !NN && b_k(i) + c >= left;
-          const bool bad = (v[c >> 1] & half_mask & 0x7f807f80u) == (half_mask & 0x7f807f80u);
-          odd |= bad && !past;
-          change |= bad || past;
-          v[c >> 1] &= bad || past ? ~half_mask : 0xffffffffu;
-        }
-        if (change) *p = v;
-      }
-      if (odd) atomicOr(&s_bits[0], 1u);
+      clean(buf, first, count, r0);
       __syncthreads();
     }
 #pragma unroll 1
@@ -665,6 +727,7 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
       __syncthreads();
       if (e + 2 < exts) issue(buf, steps + e + 2);
     }
+  }
   }
   // The tile leaves through LDS (rows of BN bf16, 16-byte chunks XOR-swizzled by the row), so
   // that neighbouring lanes store neighbouring bytes.

@@ -261,6 +261,49 @@ def test_many_adapters_interleaved_in_a_long_batch(T):
     c.check_forward(*c.forward())
 
 
+@pytest.mark.parametrize("R", [8, 16, 24, 32, 40, 64, 72, 128])
+@pytest.mark.parametrize("T,N", [(330, 4104), (2049, 1032)])
+def test_adapters_side_by_side_in_a_step(T, N, R):
+    """Mixed requests in tiles: several small adapters to a step of the expand, one large one over two."""
+    say(f"[project] mixed T={T} N={N} R={R}")
+    c = Case(T, 200, N, 11, R, mixed=True)
+    c.check_forward(*c.forward())
+    c.check_backward(c.backward(want=("dx",)), want=("dx",))
+
+
+@pytest.mark.parametrize("T,N", [(5, 40), (16, 4104), (16, 8200), (20, 2056), (31, 4104), (40, 1032), (60, 2056),
+                                 (40, 4104), (100, 4104), (130, 4104), (250, 2056)])
+def test_few_tokens_in_every_tile(T, N):
+    say(f"[project] few T={T} N={N}")
+    c = Case(T, 328, N, 9, 24)
+    c.check_forward(*c.forward())
+
+
+@pytest.mark.parametrize("T,N", [(600, 4104), (300, 1000)])
+def test_an_odd_adapter_among_others_of_its_step(T, N):
+    """An adapter whose B and A hold infinities and NaN shares steps of the expand, forward and backward, with others:
+    other requests' rows do not change, and its own are not finite where its adapter is not."""
+    c = Case(T, 128, N, 6, 16, mixed=True, dirty=False)
+    c.rank[:] = 16
+    c.pool.rank.fill_(16)
+    y = c.forward()[0].clone()
+    dx = c.backward(want=("dx",))["dx"].clone()
+    c.b[4, 17, 3], c.b[4, N - 1, 15], c.a[4, 5, 77] = float("inf"), float("nan"), float("-inf")
+    y2 = c.forward()[0]
+    other = torch.from_numpy(c.slot != 4).to(dev())
+    assert torch.equal(y[other], y2[other])
+    assert not torch.isfinite(y2[~other]).any()  # (a whole row of A x is infinite)
+    c.a[4, 5, 77] = 0.0
+    y3 = c.forward()[0]
+    assert not torch.isfinite(y3[~other][:, [17, N - 1]]).any()
+    assert torch.isfinite(y3[~other][:, :17]).all() and torch.isfinite(y3[~other][:, 18:N - 1]).all()
+    c.b[4], c.a[4, 5, 77] = 0.0, float("inf")  # u is 0: 0 * inf in column 77 of its own rows alone
+    dx2 = c.backward(want=("dx",))["dx"]
+    assert torch.equal(dx[other], dx2[other])
+    assert not torch.isfinite(dx2[~other][:, 77]).any()
+    assert torch.isfinite(dx2[~other][:, :77]).all() and torch.isfinite(dx2[~other][:, 78:]).all()
+
+
 @pytest.mark.parametrize("T", [33, 400])
 def test_no_adapter_at_all(T):
     c = Case(T, 96, 136, 2, 16)
