@@ -610,17 +610,17 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
   if constexpr (kRing) {
     constexpr int kLoads = A_IT + B_IT;  // of a wavefront for one step, whichever it is
     const int total = steps + exts;
-    issue(1, 1);
-    issue(2, 2);
+#pragma unroll 1
+    for (int s = 1; s < NB - 1; ++s) issue(s, s);
 #pragma unroll 1
     for (int s = 0; s < total; ++s) {
-      if (s + 2 < total)
-        dma_wait<2 * kLoads>();
+      if (s + NB - 2 < total)
+        dma_wait<(NB - 2) * kLoads>();
       else
         dma_wait_all();
       __syncthreads();
-      issue((s + 3) & 3, s + 3);
-      const int buf = s & 3;
+      issue((s + NB - 1) & (NB - 1), s + NB - 1);
+      const int buf = s & (NB - 1);
       int left = 64;
       if (s >= steps) {
         int first, count, r0;
@@ -818,11 +818,19 @@ int launch_tiles(const ProjectArgs &a, hipStream_t s) {
   return ok();
 }
 
+// The largest tiles that still come to most of a round of workgroups; 32 x 32 while all of
+// those run at once, two to a compute unit (dx with adapters, 64 tokens, 4096 -> 2048: 40.4 us
+// in tiles of 64, 28.5 of 32; 512 tokens, 2048 -> 1024, 512 tiles of 32: 21.4 and 19.5; 512,
+// 4096 -> 2048, 1024 tiles: 33.5 and 45).
 template <bool NN>
 int launch_product(const ProjectArgs &a, hipStream_t s) {
   auto tiles = [&](int b) { return (long long)((a.T + b - 1) / b) * ((a.N + b - 1) / b); };
   if (tiles(256) >= 192) return launch_tiles<256, 256, 2, 2, NN>(a, s);
   if (tiles(128) >= 160) return launch_tiles<128, 128, 2, 2, NN>(a, s);
+  // (calls of the forward form with fewer tiles go to the few-token kernel)
+  if constexpr (NN) {
+    if (tiles(32) <= 512) return launch_tiles<32, 32, 2, 2, NN>(a, s);
+  }
   return launch_tiles<64, 64, 2, 2, NN>(a, s);
 }
 
