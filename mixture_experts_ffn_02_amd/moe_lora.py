@@ -316,6 +316,7 @@ class AdapterPool:
     _c: _lib.Pool = field(init=False, repr=False, compare=False)
     _shape: tuple = field(init=False, repr=False, compare=False)
     _at: tuple = field(init=False, repr=False, compare=False)
+    _device: int = field(init=False, repr=False, compare=False)
 
     def __post_init__(self):
         if self.a.dim() != 3 or self.b.dim() != 3:
@@ -330,10 +331,20 @@ class AdapterPool:
             _checked("a", self.a, bf16, S * R * K), _checked("b", self.b, bf16, S * N * R)))
         object.__setattr__(self, "_shape", (T, K, N))
         object.__setattr__(self, "_at", self._addresses())
+        devices = {t.get_device() for t in (self.token_slot, self.rank, self.scaling, self.a, self.b)}
+        if len(devices) != 1:
+            raise ValueError("the tensors of a pool are on different devices")
+        object.__setattr__(self, "_device", devices.pop())
 
     def _addresses(self):
         return (self.token_slot.data_ptr(), self.rank.data_ptr(), self.scaling.data_ptr(), self.a.data_ptr(),
                 self.b.data_ptr())
+
+    def on(self, dev: int) -> int:
+        """dev, which has to be the pool's device."""
+        if dev != self._device:
+            raise ValueError(f"the pool is not on the call's device, cuda:{dev}")
+        return dev
 
     def with_slots(self, token_slot: torch.Tensor) -> "AdapterPool":
         return AdapterPool(token_slot, self.rank, self.scaling, self.a, self.b)
@@ -374,7 +385,7 @@ def moe_lora_project(x, w, pool: AdapterPool, y, ws, v=None, stream=None) -> Non
     p = pool.to_c(T, K, N)
     px, ldx = _matrix("x", x, T, K)
     py, ldy = _matrix("y", y, T, N)
-    _call("moe_lora_project", _on(x, w, y, ws, v, pool.token_slot, pool.rank, pool.scaling, pool.a, pool.b), stream,
+    _call("moe_lora_project", pool.on(_on(x, w, y, ws, v)), stream,
           ctypes.byref(_lib.ProjDims(T, K, N, ldx, ldy)), px, _checked("w", w, torch.bfloat16, N * K),
           ctypes.byref(p), py, None if v is None else _checked("v", v, torch.float32, T * p.max_rank),
           *_workspace(ws))
@@ -397,8 +408,7 @@ def moe_lora_project_backward(dy, w, pool: AdapterPool, v, ws, x=None, x_codes=N
     px, ldx = (None, K) if x is None else _matrix("x", x, T, K)
     pdy, ldy = _matrix("dy", dy, T, N)
     _call("moe_lora_project_backward",
-          _on(dy, w, v, ws, x, x_codes, x_exps, dx, da, db, pool.token_slot, pool.rank, pool.scaling, pool.a, pool.b),
-          stream, ctypes.byref(_lib.ProjDims(T, K, N, ldx, ldy)), px,
+          pool.on(_on(dy, w, v, ws, x, x_codes, x_exps, dx, da, db)), stream, ctypes.byref(_lib.ProjDims(T, K, N, ldx, ldy)), px,
           None if x_codes is None else _checked("x_codes", x_codes, u8, T * K),
           None if x_exps is None else _checked("x_exps", x_exps, u8, T * ((K + 31) // 32)),
           _checked("w", w, bf16, N * K), ctypes.byref(p),
