@@ -34,8 +34,8 @@ constexpr int kGradCols = 128;
 
 // One workgroup: 128 columns of x (dA) or dy (dB), one adapter, RT * 16 ranks, one part of
 // the adapter's tokens; its wavefronts take pieces of 32 tokens in turn, each with the next
-// piece's rows and the token numbers of the one after it loaded ahead (4096 tokens, 2048 -> 4096, rank
-// 32: 1.4 us of the call).
+// piece's rows and the token numbers of the one after it loaded ahead (4096 tokens,
+// 2048 -> 4096, rank 32: 1.4 us of the call).
 template <int RT, bool FOR_A, bool CODES>
 MOE_DEV void adapter_grad_sum(const AdapterGradArgs &P, int c, int r0, int lo, int hi, f32x4_t (&acc)[8][RT]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane & 15, grp = lane >> 4;
