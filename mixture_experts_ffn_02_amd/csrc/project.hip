@@ -805,8 +805,8 @@ int launch_few(const ProjectArgs &a, hipStream_t s) {
 }
 
 // Whether the few-token kernel takes the call: while its widest tiles all run at once (512
-// tokens, 4096 -> 2048: 20.9 us against 32.9 in LDS tiles; 2048 -> 4096, two rounds of
-// workgroups: 23.6 against 18.9).
+// tokens, 4096 -> 2048, 8 mixed adapters: 31.7 us against 36.3 in LDS tiles; 2048 -> 4096, two
+// rounds of workgroups: 33.9 against 32.0).
 bool takes_few(const ProjectArgs &a) {
   return a.T <= 32 || (long long)((a.T + 63) / 64) * ((a.N + 63) / 64) <= 256;
 }
