@@ -142,15 +142,16 @@ MOE_DEV bool take_best(uint32_t (&hi)[N], uint32_t (&lo)[N], uint64_t lanes, uin
 }
 
 // Whether fp32 keys a >= b (order keys of values) decide as the fp64 ones do.  In half steps of
-// 2^-24, around values of at most 1: a softmax sum takes 36 at most (32 terms in a lane and
-// four joins, 512 experts on 16 lanes), exp and the division some six, so a score is off by
-// less than 2^-18.5; with groups (64 lanes: 8 terms and six joins) by less than 2^-19.5, and a
-// sum of two keys by 2^-18.5.  Adding the bias takes a half step of the key.  A difference
-// above 2^-17 + 2^-20 of the keys is larger than two such errors.  Ties and what is not
-// finite are not decided.
-MOE_DEV bool decided(uint32_t a, uint32_t b) {
+// 2^-24, around values of at most 1: exp and the division take some six (a sigmoid is off by
+// less than 2^-21.4, a sum of two by 2^-20.4), a softmax sum 36 at most (32 terms in a lane and
+// four joins, 512 experts on 16 lanes), so a softmax score is off by less than 2^-18.5; with
+// groups (64 lanes: 8 terms and six joins) by less than 2^-19.5, and a sum of two keys by
+// 2^-18.5.  Adding the bias takes a half step of the key.  A difference above slack (2^-19 of
+// sigmoids, 2^-17 else) + 2^-20 of the keys is larger than two such errors.  Ties and what is
+// not finite are not decided.
+MOE_DEV bool decided(uint32_t a, uint32_t b, float slack) {
   const float x = key_f32(a), y = key_f32(b);
-  return x - y > 0x1p-17f + 0x1p-20f * fmaxf(fabsf(x), fabsf(y)) && fabsf(x) < 1e30f;
+  return x - y > slack + 0x1p-20f * fmaxf(fabsf(x), fabsf(y)) && fabsf(x) < 1e30f;
 }
 
 // orders one wavefront's own LDS writes and reads
@@ -228,6 +229,7 @@ __global__ __launch_bounds__(kRouteThreads) void scored_kernel(const ScoredParam
   const uint64_t lanes = LPT == 64 ? ~0ull : (0xffffull << (lane & 48));
   const uint64_t lower = lanes & ((1ull << lane) - 1);
   const bool sigmoid = s.score == MOE_LORA_SCORE_SIGMOID;
+  const float slack = sigmoid ? 0x1p-19f : 0x1p-17f;
   const bool grouped = LPT == 64 && a.n_group > 1;  // (groups run on whole wavefronts)
 
   for (int t0 = w_begin; t0 < w_end; t0 += TPW) {
@@ -342,7 +344,7 @@ __global__ __launch_bounds__(kRouteThreads) void scored_kernel(const ScoredParam
         for (int r = 0; r < a.topk_group; ++r)
           kept |= __ballot(take_best<64, 1, F64>(gh, gl, ~0ull, (1ull << lane) - 1, m, at));  // the groups' first lanes
         if constexpr (WIDE && !F64) {
-          if (a.topk_group < a.n_group) sure = decided(m, lanes_max_u32<64>(gh[0]));
+          if (a.topk_group < a.n_group) sure = decided(m, lanes_max_u32<64>(gh[0]), slack);
         }
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
@@ -352,7 +354,7 @@ __global__ __launch_bounds__(kRouteThreads) void scored_kernel(const ScoredParam
         }
         __builtin_amdgcn_wave_barrier();
       }
-      uint32_t last = 0;
+      uint32_t taken = 0;  // lane j of the token: its j-th key
       for (int j = 0; j < K; ++j) {
         int at = 0;
         uint32_t m;
@@ -363,10 +365,7 @@ __global__ __launch_bounds__(kRouteThreads) void scored_kernel(const ScoredParam
         } else if (own && tv) {
           id_row[j] = ll * EPL + at;
         }
-        if constexpr (WIDE && !F64) {
-          if (s.bias && j > 0) sure = sure && decided(last, m);
-          last = m;
-        }
+        if constexpr (WIDE && !F64) taken = ll == j ? m : taken;
       }
       if constexpr (WIDE && !F64) {
         if (s.bias) {
@@ -374,7 +373,10 @@ __global__ __launch_bounds__(kRouteThreads) void scored_kernel(const ScoredParam
 #pragma unroll
           for (int i = 1; i < EPL; ++i) best = hi[i] > best ? hi[i] : best;
           best = lanes_max_u32<LPT>(best);
-          sure = sure && (best == 0u || decided(last, best));
+          // each key taken against the next, the last against the best that is left
+          uint32_t next = (uint32_t)__shfl((int)taken, lane + 1);
+          next = ll == K - 1 ? best : next;
+          sure = sure && (ll >= K || (ll == K - 1 && best == 0u) || decided(taken, next, slack));
         }
       }
       return sure;
