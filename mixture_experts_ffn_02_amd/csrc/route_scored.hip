@@ -147,8 +147,8 @@ MOE_DEV bool take_best(uint32_t (&hi)[N], uint32_t (&lo)[N], uint64_t lanes, uin
 // four joins, 512 experts on 16 lanes), so a softmax score is off by less than 2^-18.5; with
 // groups (64 lanes: 8 terms and six joins) by less than 2^-19.5, and a sum of two keys by
 // 2^-18.5.  Adding the bias takes a half step of the key.  A difference above slack (2^-19 of
-// sigmoids, 2^-17 else) + 2^-20 of the keys is larger than two such errors.  Ties and what is
-// not finite are not decided.
+// sigmoids, 2^-17 else; of sums, and 2^-20 of the largest key in one) + 2^-20 of the keys is
+// larger than two such errors.  Ties and what is not finite are not decided.
 MOE_DEV bool decided(uint32_t a, uint32_t b, float slack) {
   const float x = key_f32(a), y = key_f32(b);
   return x - y > slack + 0x1p-20f * fmaxf(fabsf(x), fabsf(y)) && fabsf(x) < 1e30f;
@@ -344,7 +344,10 @@ __global__ __launch_bounds__(kRouteThreads) void scored_kernel(const ScoredParam
         for (int r = 0; r < a.topk_group; ++r)
           kept |= __ballot(take_best<64, 1, F64>(gh, gl, ~0ull, (1ull << lane) - 1, m, at));  // the groups' first lanes
         if constexpr (WIDE && !F64) {
-          if (a.topk_group < a.n_group) sure = decided(m, lanes_max_u32<64>(gh[0]), slack);
+          // (keys of opposite sign may leave a small sum: their own roundings count)
+          const float size = head && s.group_score == 2 ? fmaxf(fabsf((float)b0), per > 1 ? fabsf((float)b1) : 0.f) : 0.f;
+          if (a.topk_group < a.n_group)
+            sure = decided(m, lanes_max_u32<64>(gh[0]), slack + 0x1p-20f * lanes_max<64>(size));
         }
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {

@@ -116,6 +116,17 @@ def test_near_ties_fall_to_the_fp64_keys():
     check_route(t, l, k, scoring("sigmoid", True, bias, n_group=8, topk_group=3, group_score=1), bias)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_group_sums_that_cancel(score):
+    """Groups of one forced and one banned expert: their sums of two are small, the fp32 roundings of the keys (3e-5 and
+    more from 1000 on) are not, and the experts' own keys lie far apart."""
+    T, E = 600, 16
+    g = np.random.Generator(np.random.PCG64(21))
+    t = torch.from_numpy((g.standard_normal((T, E)) * 0.01).astype(np.float32))
+    bias = np.float32([1000.0, -1000.0] * np.arange(1, E // 2 + 1)[:, None]).ravel()
+    check_route(t, t.double().numpy(), 4, scoring(score, True, bias, n_group=8, topk_group=4, group_score=2), bias)
+
+
 def test_not_finite_logits_keep_the_ids_valid():
     t, _ = make_logits(66, 96, "f32", 4)
     t[0, 7] = float("nan")
