@@ -15,8 +15,9 @@
 // renormalised (nothing underflows in the sum).  The expert-sorted pack is the one of
 // moe_lora_route.
 //
-// Bound: at 1 to 64 tokens one workgroup's latency (one launch); above, the selection's
-// vector instructions (two launches).
+// Bound: at 1 to 64 tokens one workgroup's latency (one launch; 1 token, 256 experts, sigmoid,
+// bias, 4 of 8 groups: 8.5 us); above, the selection's vector instructions (two launches;
+// 16384 tokens, 128 experts, softmax: 11 + 5 us).
 #include <type_traits>
 
 #include "common.h"
@@ -430,7 +431,7 @@ __global__ __launch_bounds__(kRouteThreads) void scored_kernel(const ScoredParam
 //   sigmoid, renorm     dl_{id_j} += c q_j (1 - s_j) (g_j - sum_i q_i g_i),  q = s / sum s
 // The k terms of a token meet in an LDS row of E floats: of equal ids the first lane writes
 // their sum (taken in j order, so results do not depend on timing), and the row leaves as
-// whole vectors.  Bound by the T x E traffic.
+// whole vectors.  Bound by latency (8192 x 128 fp32, 8.9 MB: 5 us).
 template <int LPT, int VEC, int CH>
 __global__ __launch_bounds__(256) void scored_backward_kernel(const ScoredBackwardArgs P) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
