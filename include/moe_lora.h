@@ -395,8 +395,8 @@ int moe_lora_finalize_backward(const moe_lora_dims *dims, const uint16_t *d_out,
  * request beside it (the layers around the experts: attention projections, a shared
  * expert), for many resident adapters:
  *   a = token_slot[t];  v[t] = A[a] x[t];  y[t] = W x[t] + [a valid] scaling[a] * B[a] v[t]
- * bf16 matrices, fp32 sums; scaling * v is rounded to bf16 once before the second product
- * (as in the expert layer), y once.
+ * bf16 matrices, fp32 sums; scaling * v enters the second product as two bf16 terms (off by
+ * at most 2^-16 of it), and y is rounded once.
  *   x [T, in] rows ldx apart, w [out, in], y [T, out] rows ldy apart (columns between are
  *   left as they were), v [T, max_rank] fp32: A x unscaled, zero past a row's rank; written
  *   if not NULL (a backward pass takes it).
@@ -438,7 +438,7 @@ int moe_lora_project(const moe_lora_proj_dims *dims, const uint16_t *x, const ui
  *   dx[t] = W^T dy[t] + A[a]^T u[t]                               [T, in], rows in apart
  *   da[s] = sum over the tokens of s of u[t] x[t]^T               [num_slots, max_rank, in]
  *   db[s] = scaling[s] * sum over them of dy[t] v[t]^T            [num_slots, out, max_rank]
- * all bf16, sums in fp32 (u enters dx rounded to bf16, da and db with 16 bits), every element
+ * all bf16, sums in fp32 (u enters dx, and u and v enter da and db, as two bf16 terms), every element
  * written: zeros for adapters without tokens and past an adapter's rank.  Repeated calls
  * give the same bits.  Where the formula meets an infinity, da and db hold an infinity or
  * NaN.  dx, da and db may each be NULL (not wanted; not all three).

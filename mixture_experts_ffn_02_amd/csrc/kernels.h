@@ -91,8 +91,8 @@ struct ShrinkArgs {
   int ldx, T, K;
   const uint16_t *m;  // A [S, R, K], or B [S, K, R]
   PoolView pool;
-  uint16_t *out_bf16;  // [T, R]
-  float *out_f32;      // [T, R] or NULL
+  uint16_t *out_terms;  // [T, 2, R]: the first bf16 terms of a token, then the second
+  float *out_f32;       // [T, R] or NULL
   // where not NULL: the tokens by adapter [T] and the adapters' first places [S + 1], made by
   // a workgroup of the same launch
   int32_t *order, *seg;
@@ -103,7 +103,7 @@ struct ProjectArgs {
   const uint16_t *w;
   PoolView pool;
   const uint16_t *a_or_b;  // the shrink's matrices
-  const uint16_t *ext_a;   // bf16 [T, R], the shrink's result
+  const uint16_t *ext_a;   // the shrink's terms, [T, 2, R]
   const uint16_t *ext_b;   // the expand's matrices
   uint16_t *y;
   int ldy;

@@ -91,6 +91,16 @@ MOE_DEV void wave_lds_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// A value as two bf16 terms: of finite values the pair is off by at most 2^-16 of the value;
+// one that bf16 holds as an infinity, and a NaN, has a second term of 0 (so that inf * b keeps
+// its sign).  Stored at rank r of a token's terms: R first ones, then R second.
+MOE_DEV void store_terms(uint16_t *terms, int R, int r, float v) {
+  const uint32_t hi = f32_to_bf16(v);
+  const float rest = (hi & 0x7f80u) == 0x7f80u ? 0.f : v - bf16_to_f32(hi);
+  terms[r] = (uint16_t)hi;
+  terms[R + r] = (uint16_t)f32_to_bf16(rest);
+}
+
 // slot of a token with an adapter of positive rank, else -1; its rank
 MOE_DEV int adapter_of(const PoolView &P, int t, int &rank) {
   const int s = P.token_slot[t];

@@ -2,13 +2,14 @@
 //
 //   v_t = A_a x_t,   y_t = W x_t + s_a B_a v_t,   a = token_slot[t]
 //
-// Two launches.  The shrink writes v (fp32, if the caller keeps it) and bf16(s_a v): 16
-// tokens and one adapter per workgroup, K split over its wavefronts and joined in LDS.  The
-// rounding of s_a v to bf16 feeds the matrix cores and is the expert layer's own (its
-// error is 2^-9 of the delta, below the rounding of y).  The product appends the expand to
-// its K loop: one step per 64 ranks of the adapters among the tile's rows, with the rows of
-// the other adapters masked.  Rows keep token order; requests of a prompt are runs of tokens,
-// so a tile meets few adapters.
+// Two launches.  The shrink writes v (fp32, if the caller keeps it) and s_a v for the matrix
+// cores, as two bf16 terms: 16 tokens and one adapter per workgroup, K split over its
+// wavefronts and joined in LDS.  The terms hold s_a v to 2^-16 of it, the size of the fp32
+// sums' own error; one rounding to bf16 would move y where the delta is not small beside W x.
+// The product appends the expand to its K loop: two steps, one for each term, per 64 ranks of
+// the adapters among the tile's rows (one step where they come to 32), with the rows of the
+// other adapters masked.  Rows keep token order; requests of a prompt are runs of tokens, so a
+// tile meets few adapters.
 //
 // Small calls (a few tokens, or few output tiles) are bound by the weights' stream and
 // latency: workgroups of 16 to 64 output columns, K split over eight wavefronts.  Larger ones
@@ -21,8 +22,8 @@ namespace {
 // ------------------------------------------------------------------------ shrink
 // out[t, r] = sum_k x[t, k] m[slot][...] over a 16-token tile, for its j-th, (j + J)-th ...
 // distinct adapter.  TR = 0: m is A [S, R, K] (k contiguous); TR = 1: m is B [S, K, R] (r
-// contiguous: read back transposed from LDS).  Stores s * out in bf16, and fp32 out (scaled
-// if TR) where wanted, zeros past the rank.  Each wavefront takes a run of 64-wide K steps, G
+// contiguous: read back transposed from LDS).  Stores the terms of s * out, and fp32 out
+// (scaled if TR) where wanted, zeros past the rank.  Each wavefront takes a run of 64-wide K steps, G
 // of them in flight, loaded with neighbouring lanes on neighbouring bytes and turned into
 // MFMA operands through LDS of its own.
 constexpr int kShrinkWaves = 8;
@@ -83,7 +84,7 @@ __global__ __launch_bounds__(kShrinkWaves * 64, LONG && MT == 1 ? 3 : 2) void sh
     for (int i = tid; i < ROWS * R; i += kShrinkWaves * 64) {
       const int r = i / R, t = t0 + r;
       if (t < P.T && s_slot[r] < 0) {
-        P.out_bf16[(size_t)t * R + i % R] = 0;
+        store_terms(P.out_terms + (size_t)t * 2 * R, R, i % R, 0.f);
         if (P.out_f32) P.out_f32[(size_t)t * R + i % R] = 0.f;
       }
     }
@@ -188,7 +189,7 @@ __global__ __launch_bounds__(kShrinkWaves * 64, LONG && MT == 1 ? 3 : 2) void sh
         for (int w = 0; w < kShrinkWaves; ++w) v += part[(w * ROWS + tr) * RP + rc];
         if (s_slot[tr] != slot || r >= R) continue;
         if (r >= rank) v = 0.f;
-        P.out_bf16[(size_t)t * R + r] = (uint16_t)f32_to_bf16(scale * v);
+        store_terms(P.out_terms + (size_t)t * 2 * R, R, r, scale * v);
         if (P.out_f32) P.out_f32[(size_t)t * R + r] = TR ? scale * v : v;
       }
     }
@@ -198,7 +199,7 @@ __global__ __launch_bounds__(kShrinkWaves * 64, LONG && MT == 1 ? 3 : 2) void sh
       for (int c = tid; c < ROWS * (R - done); c += kShrinkWaves * 64) {
         const int tr = c / (R - done), t = t0 + tr, r = done + c % (R - done);
         if (s_slot[tr] != slot) continue;
-        P.out_bf16[(size_t)t * R + r] = 0;
+        store_terms(P.out_terms + (size_t)t * 2 * R, R, r, 0.f);
         if (P.out_f32) P.out_f32[(size_t)t * R + r] = 0.f;
       }
     }
@@ -258,15 +259,17 @@ __global__ __launch_bounds__(W * 64) void project_few_kernel(const ProjectArgs P
 
   // the expand: 32 ranks of Q adapters' rows at a time
   constexpr int Q = 2;
-  u32x4_t vf[FM], bf[Q][FN];
+  u32x4_t vf[FM][2], bf[Q][FN];
   int slot[Q], rank[Q];
   auto load_v = [&](int r0) {
     const int r = r0 + grp * 8;
 #pragma unroll
     for (int i = 0; i < FM; ++i)
-      vf[i] = r < pool.R ? *reinterpret_cast<const u32x4_t *>(
-                               P.ext_a + (size_t)min(t0 + i * 16 + row, P.T - 1) * pool.R + r)
-                         : zero_u32x4();
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        vf[i][h] = r < pool.R ? *reinterpret_cast<const u32x4_t *>(
+                                    P.ext_a + ((size_t)min(t0 + i * 16 + row, P.T - 1) * 2 + h) * pool.R + r)
+                              : zero_u32x4();
   };
   auto load_b = [&](int r0, int q0) {
     const int r = r0 + grp * 8;
@@ -339,7 +342,8 @@ __global__ __launch_bounds__(W * 64) void project_few_kernel(const ProjectArgs P
           for (int i = 0; i < FM; ++i)
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
-              const f32x4_t d = mfma_16x16x32(bf[q][j], vf[i], acc[i][j]);
+              f32x4_t d = mfma_16x16x32(bf[q][j], vf[i][0], acc[i][j]);
+              d = mfma_16x16x32(bf[q][j], vf[i][1], d);
               if (slot_row[i] == slot[q]) acc[i][j] = d;
             }
         }
@@ -472,29 +476,44 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
     for (int i = 0; i < B_IT; ++i)
       dma16(k0 + b_k(i) < K ? bb + b_off[i] : reinterpret_cast<const char *>(kZeroChunk), b_lds(buf) + i * NT * 16);
   };
-  // A step of the expand holds `per` adapters of up to 32 ranks side by side, or 64 ranks of
-  // one: ranks [r0, r0 + 64) of the adapters at [first, first + count) of the list.  (A step
+  // A group of the expand holds `per` adapters of up to 32 ranks side by side, or 64 ranks of
+  // one: ranks [r0, r0 + 64) of the adapters at [first, first + count) of the list.  (A group
   // for each adapter: 8192 tokens of 8 mixed adapters of rank 16, 2048 -> 4096: 230 us, 179
-  // so; dx of 64 tokens of 32 adapters 61 us, 40 so.)
+  // so; dx of 64 tokens of 32 adapters 61 us, 40 so.)  It takes two steps over the same rows
+  // of B: the first terms of s v, then the second.  Where all of the tile's adapters come to
+  // 32 ranks (packed) one step does: A holds the first terms in its lower half and the second
+  // in its upper, and both meet B's lower half.
   const int R = pool.R, per = R <= 32 ? 64 / R : 1;
-  // reduction index k of a step: its adapter (slot | rank << 16) and rank there; false: none
+  bool packed = false;  // known once the adapters are listed
+  const uint32_t inv = (65536u + R - 1) / R;  // k / R = k inv >> 16 for k < 64 (R >= 8: off by less than 1 / R)
+  // reduction index k of a group: its adapter (slot | rank << 16) and rank there; false: none
   auto ext_at = [&](int first, int count, int r0, int k, int &entry, int &r) MOE_INLINE {
-    const int j = per > 1 ? k / R : 0;
+    const int j = per > 1 ? (int)((uint32_t)k * inv >> 16) : 0;
     r = r0 + k - j * R;
     entry = s_list[first + min(j, count - 1)];
     return j < count && r < list_rank(entry);
   };
-  auto issue_ext = [&](int buf, int first, int count, int r0) MOE_INLINE {
-    const char *z = reinterpret_cast<const char *>(kZeroChunk);
+  // a term of a group's s v into buf, and where buf2 >= 0 the next one into buf2
+  auto issue_ext_a = [&](int buf, int buf2, int first, int count, int r0, int term) MOE_INLINE {
     static_assert(NT % 64 == 0, "a thread's chunks of rows of 64 are at one reduction index");
     int entry, r;
-    const bool live = ext_at(first, count, r0, a_k(0), entry, r);
+    const int k = packed ? a_k(0) & 31 : a_k(0);
+    if (packed) term = a_k(0) >> 5;
+    const bool live = ext_at(first, count, r0, k, entry, r);
+    const uint16_t *src = P.ext_a + (size_t)t0 * 2 * R + term * R + r;
 #pragma unroll
     for (int i = 0; i < A_IT; ++i) {
       const int t = (i * NT + tid) >> 3;
       const bool on = live && s_slot[t] == list_slot(entry);
-      dma16(on ? reinterpret_cast<const char *>(P.ext_a + (size_t)(t0 + t) * R + r) : z, a_lds(buf) + i * NT * 16);
+      const void *z = kZeroChunk, *p = src + (size_t)t * 2 * R;
+      dma16(on ? p : z, a_lds(buf) + i * NT * 16);
+      if (buf2 >= 0) dma16(on ? static_cast<const uint16_t *>(p) + R : z, a_lds(buf2) + i * NT * 16);
     }
+  };
+  auto issue_ext_b = [&](int buf, int first, int count, int r0) MOE_INLINE {
+    const char *z = reinterpret_cast<const char *>(kZeroChunk);
+    int entry, r;
+    const bool live = ext_at(first, count, r0, a_k(0), entry, r);
 #pragma unroll
     for (int i = 0; i < B_IT; ++i) {
       const char *src = z;
@@ -516,31 +535,31 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  int a_frag[2], b_frag[2];
-#pragma unroll
-  for (int kk = 0; kk < 2; ++kk) {
-    a_frag[kk] = row * 64 + (((kk * 4 + grp) ^ (row & 7)) << 3);
-    b_frag[kk] = a_frag[kk];
-  }
+  // a lane's chunk of a half kk in rows of 64: chunk (4 kk + grp) ^ (row % 8) of row `row`
+  const int frag0 = row * 64 + ((grp ^ (row & 7)) << 3);
+  auto frag = [&](int kk) MOE_INLINE { return frag0 ^ (kk << 5); };
   // NN: lane's row of a transposed read is 32 kk + 8 grp + row / 4 (+ 4), whose swizzle is
   // (row / 4) | 4 (grp & 1); columns 4 (row % 4) of a 16-wide piece (one 32-byte pair)
   const int tr_row = grp * 8 + (row >> 2), tr_swz = ((row >> 2) | ((grp & 1) << 2)) & SWZ;
 
   // the c-th of the reads that bring one 32-wide half's operands into registers
   constexpr int kReads = FM + (NN ? 2 * FN : FN);
-  auto read = [&](int buf, int kk, int c, u32x4_t(&af)[FM], u32x4_t(&bf)[FN]) MOE_INLINE {
+  auto read2 = [&](int a_buf, int a_kk, int b_buf, int b_kk, int c, u32x4_t(&af)[FM], u32x4_t(&bf)[FN]) MOE_INLINE {
     if (c < FM) {
-      af[c] = *reinterpret_cast<const u32x4_t *>(&As[buf][(wm * WTM + c * 16) * 64 + a_frag[kk]]);
+      af[c] = *reinterpret_cast<const u32x4_t *>(&As[a_buf][(wm * WTM + c * 16) * 64 + frag(a_kk)]);
     } else if constexpr (!NN) {
-      bf[c - FM] = *reinterpret_cast<const u32x4_t *>(&Bs[buf][(wn * WTN + (c - FM) * 16) * 64 + b_frag[kk]]);
+      bf[c - FM] = *reinterpret_cast<const u32x4_t *>(&Bs[b_buf][(wn * WTN + (c - FM) * 16) * 64 + frag(b_kk)]);
     } else {
       const int j = (c - FM) >> 1, h = (c - FM) & 1;
       const int pair = (wn * WTN) / 16 + j;
       const u32x2_t v = lds_read_tr(
-          &Bs[buf][(kk * 32 + tr_row + 4 * h) * BN + ((pair ^ tr_swz) << 4) + 4 * (row & 3)]);
+          &Bs[b_buf][(b_kk * 32 + tr_row + 4 * h) * BN + ((pair ^ tr_swz) << 4) + 4 * (row & 3)]);
       bf[j][2 * h] = v[0];
       bf[j][2 * h + 1] = v[1];
     }
+  };
+  auto read = [&](int buf, int kk, int c, u32x4_t(&af)[FM], u32x4_t(&bf)[FN]) MOE_INLINE {
+    read2(buf, kk, buf, kk, c, af, bf);
   };
 
   // Pipeline of a step: its first half's operands are in registers when it begins; the
@@ -550,29 +569,40 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
   // of the next step's first operands.  (DMA loads in one burst instead held the products
   // up: 8192 x 2048 -> 4096 in 137 us against 129, dx of 4096 x 4096 -> 2048 in 69 against 61.)
   const int steps = (K + 63) / 64, full = K / 64;
-  const int chunks = (R + 63) / 64;  // steps of an adapter of more than 32 ranks
-  int adapters = 0, exts = 0;        // known once the adapters are listed
-  // the e-th step of the expand; left: its reduction's length (may be 0 or less)
+  // groups of an adapter of more than 32 ranks: 1 << two
+  static_assert(MOE_LORA_MAX_POOL_RANK <= 128, "two groups at most");
+  const int two = R > 64 ? 1 : 0;
+  int adapters = 0, exts = 0;        // (exts: steps of the expand) known once the adapters are listed
+  // the e-th group of the expand; left: its reduction's length (may be 0 or less)
   auto ext_of = [&](int e, int &first, int &count, int &r0, int &left) MOE_INLINE {
-    first = per > 1 ? e * per : e / chunks;
+    first = per > 1 ? e * per : e >> two;
     count = min(per, adapters - first);
-    r0 = per > 1 ? 0 : (e - first * chunks) * 64;
+    r0 = per > 1 ? 0 : (e & two) * 64;
     left = per > 1 ? count * R : list_rank(__builtin_amdgcn_readfirstlane(s_list[first])) - r0;
   };
+  // step h of the expand: its group and term.  Its A goes where any step's does; a group's B,
+  // which two steps read, into the buffer of its own count (free: the step that had it before
+  // is at least a buffer's turn behind).
+  auto group_of = [&](int h) MOE_INLINE { return packed ? h : h >> 1; };
+  auto term_of = [&](int h) MOE_INLINE { return packed ? 0 : h & 1; };
+  auto ext_b_buf = [&](int h) MOE_INLINE { return (steps + group_of(h)) & (NB - 1); };
   auto issue = [&](int buf, int s) MOE_INLINE {
     if (s < full) {
       issue_full(buf, s * 64);
     } else if (s < steps) {
       issue_tail(buf, s * 64);
     } else if (s < steps + exts) {
+      const int h = s - steps;
       int first, count, r0, left;
-      ext_of(s - steps, first, count, r0, left);
-      issue_ext(buf, first, count, r0);
+      ext_of(group_of(h), first, count, r0, left);
+      issue_ext_a(buf, -1, first, count, r0, term_of(h));
+      if (term_of(h) == 0) issue_ext_b(ext_b_buf(h), first, count, r0);
     }
   };
   issue(0, 0);
   adapters = tile_adapters<BM, NT>(pool, t0, P.T, s_slot, s_list, s_bits);
-  exts = per > 1 ? (adapters + per - 1) / per : chunks * adapters;
+  packed = adapters * R <= 32;
+  exts = (per > 1 ? (adapters + per - 1) / per : adapters << two) * (packed ? 1 : 2);
   if (tid == 0) s_bits[0] = 0u;  // from here on: whether an adapter holds what is not finite
   // The expand.  Other requests' rows of the A operand are zeros; so that nothing that an
   // adapter holds reaches them as 0 * inf or 0 * NaN, what is not finite in its rows is taken
@@ -589,6 +619,11 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
     for (int i = 0; i < B_IT; ++i) {
       u32x4_t *p = reinterpret_cast<u32x4_t *>(&Bs[buf][(i * NT + tid) * 8]);
       u32x4_t v = *p;
+      // an exponent of ones carries into the sign's place
+      uint32_t ones = 0;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) ones |= (v[c] & 0x7f807f80u) + 0x00800080u;
+      if ((ones & 0x80008000u) == 0u && ranks >= 8) continue;
       bool change = false;
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
@@ -605,34 +640,52 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
     if (odd) atomicOr(&s_bits[0], 1u);
   };
   u32x4_t af1[FM], bf1[FN];
+  // the products of a step of the expand, whose A is in a_buf; left: its group's
+  auto expand = [&](int h, int a_buf, int left) MOE_INLINE {
+    const int b_buf = ext_b_buf(h);
+#pragma unroll 1
+    for (int kk = 0; kk < 2 && (packed || kk * 32 < left); ++kk) {
+#pragma unroll
+      for (int c = 0; c < kReads; ++c) read2(a_buf, kk, b_buf, packed ? 0 : kk, c, af1, bf1);
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = mfma_16x16x32(bf1[j], af1[i], acc[i][j]);
+    }
+  };
+  // clears a group's B of what is not finite before its first step
+  auto prepare_ext = [&](int h, int &left) MOE_INLINE {
+    int first, count, r0;
+    ext_of(group_of(h), first, count, r0, left);
+    if (left > 0 && term_of(h) == 0) {
+      clean(ext_b_buf(h), first, count, r0);
+      __syncthreads();
+    }
+  };
   // A small tile's steps are short beside the loads' latency: four of them in LDS, three on
   // their way (dx without adapters, 64 tokens, 4096 -> 2048: 32.1 -> 24.4 us; 512: 33 -> 25).
   if constexpr (kRing) {
-    constexpr int kLoads = A_IT + B_IT;  // of a wavefront for one step, whichever it is
+    // loads of a wavefront for one step: A_IT + B_IT, A_IT for the expand's second one
+    constexpr int kLoads = A_IT + B_IT;
+    static_assert(NB == 4, "two steps on their way behind the one that is waited for");
+    const int groups = packed ? exts : exts >> 1;
+    exts = min(exts, 2);  // the first group's go out in the main loop, the others' whole one group ahead
     const int total = steps + exts;
 #pragma unroll 1
     for (int s = 1; s < NB - 1; ++s) issue(s, s);
 #pragma unroll 1
-    for (int s = 0; s < total; ++s) {
-      if (s + NB - 2 < total)
-        dma_wait<(NB - 2) * kLoads>();
-      else
+    for (int s = 0; s < steps; ++s) {
+      if (s + NB - 2 >= total)
         dma_wait_all();
+      else if (s + NB - 2 > steps)
+        dma_wait<kLoads + A_IT>();
+      else
+        dma_wait<2 * kLoads>();
       __syncthreads();
       issue((s + NB - 1) & (NB - 1), s + NB - 1);
       const int buf = s & (NB - 1);
-      int left = 64;
-      if (s >= steps) {
-        int first, count, r0;
-        ext_of(s - steps, first, count, r0, left);
-        if (left > 0) {
-          clean(buf, first, count, r0);
-          __syncthreads();
-        }
-      }
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
-        if (kk * 32 >= left) break;
 #pragma unroll
         for (int c = 0; c < kReads; ++c) read(buf, kk, c, af1, bf1);
 #pragma unroll
@@ -640,6 +693,23 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
 #pragma unroll
           for (int j = 0; j < FN; ++j) acc[i][j] = mfma_16x16x32(bf1[j], af1[i], acc[i][j]);
       }
+    }
+    // (a group's two steps together: its addresses are found once, and one barrier serves both)
+#pragma unroll 1
+    for (int g = 0; g < groups; ++g) {
+      const int at = steps + 2 * g;
+      dma_wait_all();
+      __syncthreads();
+      if (g + 1 < groups) {
+        int first, count, r0, left;
+        ext_of(g + 1, first, count, r0, left);
+        issue_ext_a((at + 2) & (NB - 1), (at + 3) & (NB - 1), first, count, r0, 0);
+        issue_ext_b(ext_b_buf(2 * (g + 1)), first, count, r0);
+      }
+      int left;
+      prepare_ext(packed ? g : 2 * g, left);
+      expand(packed ? g : 2 * g, at & (NB - 1), left);
+      if (!packed) expand(2 * g + 1, (at + 1) & (NB - 1), left);
     }
   } else {
   dma_wait_all();
@@ -705,27 +775,15 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
   }
 
 #pragma unroll 1
-  for (int e = 0; e < exts; ++e) {
-    const int buf = (steps + e) & 1;
-    int first, count, r0, left;
-    ext_of(e, first, count, r0, left);
-    if (left > 0) {
-      clean(buf, first, count, r0);
-      __syncthreads();
-    }
-#pragma unroll 1
-    for (int kk = 0; kk < 2 && kk * 32 < left; ++kk) {
-#pragma unroll
-      for (int c = 0; c < kReads; ++c) read(buf, kk, c, af1, bf1);
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = mfma_16x16x32(bf1[j], af1[i], acc[i][j]);
-    }
-    if (e + 1 < exts) {
+  for (int h = 0; h < exts; ++h) {
+    const int buf = (steps + h) & 1;
+    int left;
+    prepare_ext(h, left);
+    expand(h, buf, left);
+    if (h + 1 < exts) {
       dma_wait_all();
       __syncthreads();
-      if (e + 2 < exts) issue(buf, steps + e + 2);
+      if (h + 2 < exts) issue(buf, steps + h + 2);
     }
   }
   }
@@ -839,7 +897,7 @@ int launch_product(const ProjectArgs &a, hipStream_t s) {
 int launch_shrink_transposed(const ShrinkArgs &a, hipStream_t s) { return launch_shrink<true>(a, s); }
 int launch_product_transposed(const ProjectArgs &a, hipStream_t s) { return launch_product<true>(a, s); }
 
-size_t project_workspace_bytes(int T, int R) { return ((size_t)T * R * 2 + 255) & ~(size_t)255; }
+size_t project_workspace_bytes(int T, int R) { return ((size_t)T * R * 4 + 255) & ~(size_t)255; }
 
 int launch_project(const ProjectArgs &a, float *v, hipStream_t s) {
   if (a.pool.S > 0) {

@@ -301,7 +301,7 @@ Layout layout_of(int T, int K, int N, int S, int R) {
     at += up(n);
     return o;
   };
-  l.ub = take((size_t)T * R * 2);
+  l.ub = take((size_t)T * R * 4);
   l.u = take((size_t)T * R * 4);
   l.order = take((size_t)T * 4);
   l.seg = take((size_t)(S + 1) * 4);
