@@ -438,7 +438,7 @@ int moe_lora_project(const moe_lora_proj_dims *dims, const uint16_t *x, const ui
  *   dx[t] = W^T dy[t] + A[a]^T u[t]                               [T, in], rows in apart
  *   da[s] = sum over the tokens of s of u[t] x[t]^T               [num_slots, max_rank, in]
  *   db[s] = scaling[s] * sum over them of dy[t] v[t]^T            [num_slots, out, max_rank]
- * all bf16, sums in fp32 (u enters dx, and u and v enter da and db, as two bf16 terms), every element
+ * all bf16, sums in fp32 (u enters dx as two bf16 terms, da and db whole), every element
  * written: zeros for adapters without tokens and past an adapter's rank.  Repeated calls
  * give the same bits.  Where the formula meets an infinity, da and db hold an infinity or
  * NaN.  dx, da and db may each be NULL (not wanted; not all three).

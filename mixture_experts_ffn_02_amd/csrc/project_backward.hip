@@ -8,8 +8,9 @@
 // together, and their parts' sums where a segment was split.  dA and dB stream x and dy once:
 // a wavefront takes 32 tokens x 128 columns as eight rows of 16 bytes per lane, turns the
 // 8 x 8 blocks in registers (v_perm), so no LDS is on the way, and multiplies by u or v,
-// whose fp32 values enter as two bf16 terms (their sum has 16 bits, so the gradients' only
-// rounding to 8 bits is their own).  Sums in fp32; an adapter's tokens are added in a fixed
+// whose fp32 values enter as three bf16 terms (all of their 24 bits, so the gradients' only
+// rounding to 8 bits is their own; the third term: 4096 tokens of four adapters of rank 32 98.8
+// -> 99.7 us for the call, of eight of rank 64 116 -> 120).  Sums in fp32; an adapter's tokens are added in a fixed
 // order.  Bound by the bytes in flight (4096 tokens, 2048 -> 4096, four adapters of rank 32,
 // x in 8 bits: 18-20 us for 42 MB, against 67 of dx and 18-20 of u).
 #include "checkpoint.h"
@@ -20,12 +21,18 @@ namespace {
 
 MOE_DEV uint32_t perm(uint32_t hi, uint32_t lo, uint32_t sel) { return __builtin_amdgcn_perm(hi, lo, sel); }
 
-// values of 8 tokens as two bf16 terms (hi + lo has 16 bits of each)
-MOE_DEV void split8(const float (&v)[8], u32x4_t &hi, u32x4_t &lo) {
+// values of 8 tokens as three bf16 terms, whose sum is the value: the top 8 bits of the 24, the
+// next 8, the rest
+MOE_DEV void split8(const float (&v)[8], u32x4_t (&t)[3]) {
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    hi[q] = pack_bf16x2(v[2 * q], v[2 * q + 1]);
-    lo[q] = pack_bf16x2(v[2 * q] - bf16_to_f32(hi[q] & 0xffffu), v[2 * q + 1] - bf16_to_f32(hi[q] >> 16));
+    float a = v[2 * q], b = v[2 * q + 1];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      t[i][q] = perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+      a -= bf16_to_f32(t[i][q] & 0xffffu);
+      b -= bf16_to_f32(t[i][q] >> 16);
+    }
   }
 }
 
@@ -112,9 +119,9 @@ MOE_DEV void adapter_grad_sum(const AdapterGradArgs &P, int c, int r0, int lo, i
 #pragma unroll
         for (int k = 0; k < RT; ++k) f[k][i] = 0.f;
       }
-    u32x4_t qh[RT], ql[RT];
+    u32x4_t q3[RT][3];
 #pragma unroll
-    for (int k = 0; k < RT; ++k) split8(f[k], qh[k], ql[k]);
+    for (int k = 0; k < RT; ++k) split8(f[k], q3[k]);
     // column j of the lane's 8 x 8 block: its 8 tokens
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -123,10 +130,10 @@ MOE_DEV void adapter_grad_sum(const AdapterGradArgs &P, int c, int r0, int lo, i
       for (int t = 0; t < 4; ++t)
         col[t] = perm(d[2 * t + 1][j >> 1], d[2 * t][j >> 1], (j & 1) ? 0x07060302u : 0x05040100u);
 #pragma unroll
-      for (int k = 0; k < RT; ++k) {
-        acc[j][k] = FOR_A ? mfma_16x16x32(col, qh[k], acc[j][k]) : mfma_16x16x32(qh[k], col, acc[j][k]);
-        acc[j][k] = FOR_A ? mfma_16x16x32(col, ql[k], acc[j][k]) : mfma_16x16x32(ql[k], col, acc[j][k]);
-      }
+      for (int k = 0; k < RT; ++k)
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          acc[j][k] = FOR_A ? mfma_16x16x32(col, q3[k][i], acc[j][k]) : mfma_16x16x32(q3[k][i], col, acc[j][k]);
     }
   }
 }

@@ -1,11 +1,12 @@
-"""The low-rank delta of the projection with pooled adapters keeps its bits: s v (and u of the gradient) enter the
-second product as two bf16 terms, not as one rounding of 2^-8."""
+"""The projection with pooled adapters keeps the bits of what lies between its products: s v (and u of the gradient)
+enter the second one as two bf16 terms, not as one rounding of 2^-8, and the adapters' gradients take u and v whole."""
 
 import numpy as np
 import pytest
 import torch
 
 from gpu_util import dev, f64, say
+from mixture_experts_ffn_02_amd import moe_lora as ml
 from oracle import operators_ref as ref
 from test_gpu_project import HALF, ULP, Case
 
@@ -87,3 +88,33 @@ def test_an_infinite_v_stays_an_infinity(T):
     assert (y[keep][:, 0::2] == 2.0).all() and (y[keep][:, 1::2] == -2.0).all()
 
 
+
+
+@pytest.mark.parametrize("codes", [False, True], ids=["bf16", "codes"])
+@pytest.mark.parametrize("T,R", [(2, 8), (70, 32), (1100, 64)])
+def test_adapter_gradients_keep_every_bit_of_u_and_v(T, R, codes):
+    """u and v of 1 + 2^-9 + 2^-18 against 1 + 2^-9: their difference, 2^-18, is what two products of opposite sign
+    leave, exact in every sum."""
+    K = N = 40
+    last = T - 1
+    bf16 = dict(dtype=torch.bfloat16, device=dev())
+    x, dy, w = torch.zeros((T, K), **bf16), torch.zeros((T, N), **bf16), torch.zeros((N, K), **bf16)
+    a, b, v = torch.zeros((1, R, K), **bf16), torch.zeros((1, N, R), **bf16), torch.zeros((T, R), device=dev())
+    i32 = dict(dtype=torch.int32, device=dev())
+    pool = ml.AdapterPool(torch.zeros(T, **i32), torch.full((1,), R, **i32), torch.ones(1, device=dev()), a, b)
+    b[0, :3, R - 1] = 1.0                                   # u: the sum of dy's first three
+    dy[0, 0], dy[0, 1], dy[0, 2] = 1.0, 2.0 ** -9, 2.0 ** -18
+    dy[last, 0], dy[last, 1] = 1.0, 2.0 ** -9
+    dy[0, 7], dy[last, 7] = 1.0, -1.0
+    x[0, 5], x[last, 5] = 1.0, -1.0
+    v[0, 3], v[last, 3] = 1.0 + 2.0 ** -9 + 2.0 ** -18, 1.0 + 2.0 ** -9
+    if codes:
+        c, e = torch.empty((T, K), dtype=torch.uint8, device=dev()), torch.empty((T, 2), dtype=torch.uint8, device=dev())
+        ml.moe_lora_checkpoint_pack(x, c, e)
+        src = dict(x_codes=c, x_exps=e)
+    else:
+        src = dict(x=x)
+    da, db = torch.full_like(a, float("nan")), torch.full_like(b, float("nan"))
+    ws = torch.empty((ml.moe_lora_project_backward_workspace_size(T, K, N, pool),), dtype=torch.uint8, device=dev())
+    ml.moe_lora_project_backward(dy, w, pool, v, ws, **src, da=da, db=db)
+    assert da[0, R - 1, 5].item() == 2.0 ** -18 and db[0, 7, 3].item() == 2.0 ** -18
