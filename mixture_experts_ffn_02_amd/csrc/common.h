@@ -49,6 +49,15 @@ MOE_DEV void store_stream(T *p, const T &v) {
 // Outputs above half of the 256 MB that the memory-side cache holds are stored past it
 constexpr size_t kStreamBytes = 128u << 20;
 
+// Workgroups over two grid dimensions: the work-items along one must stay below 2^32 (a launch
+// of more runs what is left of their count, with no error).  block_of_grid: this one's number,
+// which may lie past the last of `blocks`.
+inline dim3 grid_of_blocks(long long blocks) {
+  const long long x = blocks < (1 << 20) ? blocks : (1 << 20);
+  return dim3((unsigned)x, (unsigned)((blocks + x - 1) / x));
+}
+MOE_DEV long long block_of_grid() { return (long long)blockIdx.y * gridDim.x + blockIdx.x; }
+
 MOE_DEV int lane_id() { return __lane_id(); }
 
 MOE_DEV u32x4_t zero_u32x4() {

@@ -22,7 +22,7 @@ __global__ __launch_bounds__(kRowThreads) void permute_kernel(const uint16_t *__
                                                               uint16_t *__restrict__ x_perm, int R,
                                                               int H, int K) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int p = blockIdx.x * (kRowThreads / 64) + wave;
+  const int p = (int)block_of_grid() * (kRowThreads / 64) + wave;
   if (p >= R) return;
   const int t = p2e[p] / K;
   const u32x4_t *src = reinterpret_cast<const u32x4_t *>(x + (size_t)t * H);
@@ -35,9 +35,10 @@ __global__ __launch_bounds__(kRowThreads) void permute_kernel(const uint16_t *__
 __global__ __launch_bounds__(kRowThreads) void finalize_kernel(const uint16_t *__restrict__ y,
                                                                const float *__restrict__ w,
                                                                const int32_t *__restrict__ e2p,
-                                                               uint16_t *__restrict__ out, int H,
+                                                               uint16_t *__restrict__ out, int T, int H,
                                                                int K) {
-  const int t = blockIdx.x;
+  const int t = (int)block_of_grid();
+  if (t >= T) return;
   __shared__ int rows[MOE_LORA_MAX_TOPK];
   __shared__ float wts[MOE_LORA_MAX_TOPK];
   if (threadIdx.x < K) {
@@ -74,7 +75,8 @@ __global__ __launch_bounds__(kRowThreads) void finalize_kernel(const uint16_t *_
 template <int JN, bool CODES>
 __global__ __launch_bounds__(kRowThreads) void finalize_backward_kernel(const FinalizeBackwardArgs P) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int t = blockIdx.x, H = P.H, K = P.K;
+  const int t = (int)block_of_grid(), H = P.H, K = P.K;
+  if (t >= P.T) return;
   const int nb = (H + kCkptBlock - 1) / kCkptBlock;
   long long row[JN];
   float w[JN], dot[JN];
@@ -134,13 +136,13 @@ template <bool CODES>
 int launch_fin_bwd(const FinalizeBackwardArgs &a, hipStream_t s) {
   const int per = (a.K + 3) / 4;
   if (per <= 1)
-    finalize_backward_kernel<1, CODES><<<a.T, kRowThreads, 0, s>>>(a);
+    finalize_backward_kernel<1, CODES><<<grid_of_blocks(a.T), kRowThreads, 0, s>>>(a);
   else if (per <= 2)
-    finalize_backward_kernel<2, CODES><<<a.T, kRowThreads, 0, s>>>(a);
+    finalize_backward_kernel<2, CODES><<<grid_of_blocks(a.T), kRowThreads, 0, s>>>(a);
   else if (per <= 4)
-    finalize_backward_kernel<4, CODES><<<a.T, kRowThreads, 0, s>>>(a);
+    finalize_backward_kernel<4, CODES><<<grid_of_blocks(a.T), kRowThreads, 0, s>>>(a);
   else
-    finalize_backward_kernel<8, CODES><<<a.T, kRowThreads, 0, s>>>(a);
+    finalize_backward_kernel<8, CODES><<<grid_of_blocks(a.T), kRowThreads, 0, s>>>(a);
   return hipGetLastError() == hipSuccess ? ST_OK : ST_HIP;
 }
 
@@ -154,15 +156,15 @@ int launch_permute(const uint16_t *x, const int32_t *p2e, uint16_t *x_perm, int 
                    hipStream_t s) {
   if (R == 0) return ST_OK;
   const int rows_per_block = kRowThreads / 64;
-  permute_kernel<<<(R + rows_per_block - 1) / rows_per_block, kRowThreads, 0, s>>>(x, p2e, x_perm,
-                                                                                    R, H, K);
+  permute_kernel<<<grid_of_blocks((R + rows_per_block - 1) / rows_per_block), kRowThreads, 0, s>>>(x, p2e, x_perm, R,
+                                                                                                    H, K);
   return hipGetLastError() == hipSuccess ? ST_OK : ST_HIP;
 }
 
 int launch_finalize(const uint16_t *y_perm, const float *w, const int32_t *e2p, uint16_t *out,
                     int T, int H, int K, hipStream_t s) {
   if (T == 0) return ST_OK;
-  finalize_kernel<<<T, kRowThreads, 0, s>>>(y_perm, w, e2p, out, H, K);
+  finalize_kernel<<<grid_of_blocks(T), kRowThreads, 0, s>>>(y_perm, w, e2p, out, T, H, K);
   return hipGetLastError() == hipSuccess ? ST_OK : ST_HIP;
 }
 
