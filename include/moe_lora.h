@@ -221,7 +221,9 @@ int moe_lora_route_scored(const moe_lora_dims *dims, const moe_lora_scoring *sco
  * written) from d_weights [T, k] fp32 for the given choice topk_ids [T, k].  The choice
  * itself has no gradient and the bias takes none.  Softmax without renormalisation reaches
  * every expert; the other forms only the chosen ones.  An id outside [0, E) takes no part;
- * equal ids of one token add up.  Groups, bias and their checks do not apply here. */
+ * equal ids of one token add up.  Groups, bias and their checks do not apply here, nor does
+ * the forward call's limit of tokens (batches routed in chunks may take their gradient at
+ * once). */
 int moe_lora_route_scored_backward(const moe_lora_dims *dims, const moe_lora_scoring *scoring,
                                    const void *logits, const int32_t *topk_ids,
                                    const float *d_weights, void *d_logits, moe_lora_stream_t stream);

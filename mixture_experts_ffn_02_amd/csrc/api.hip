@@ -160,12 +160,13 @@ int check_scoring(const moe_lora_dims *d, const moe_lora_scoring *sc) {
   if (sc->logits_dtype != MOE_LORA_DTYPE_BF16 && sc->logits_dtype != MOE_LORA_DTYPE_F32)
     return MOE_LORA_ERR_INVALID_ARGUMENT;
   if (sc->renormalize != 0 && sc->renormalize != 1) return MOE_LORA_ERR_INVALID_ARGUMENT;
-  if (d->num_tokens > moe::scored_max_tokens()) return MOE_LORA_ERR_UNSUPPORTED;
   return MOE_LORA_OK;
 }
 
-int check_groups(const moe_lora_dims *d, const moe_lora_scoring *sc) {
+// what only the choice and its pack need
+int check_choice(const moe_lora_dims *d, const moe_lora_scoring *sc) {
   const int E = d->num_experts;
+  if (d->num_tokens > moe::scored_max_tokens()) return MOE_LORA_ERR_UNSUPPORTED;
   if (sc->n_group <= 0 || sc->n_group > 64 || E % sc->n_group != 0) return MOE_LORA_ERR_INVALID_ARGUMENT;
   if (sc->topk_group <= 0 || sc->topk_group > sc->n_group) return MOE_LORA_ERR_INVALID_ARGUMENT;
   if (d->top_k > sc->topk_group * (E / sc->n_group)) return MOE_LORA_ERR_INVALID_ARGUMENT;
@@ -176,7 +177,7 @@ int check_groups(const moe_lora_dims *d, const moe_lora_scoring *sc) {
 }  // namespace
 
 size_t moe_lora_route_scored_workspace_size(const moe_lora_dims *d, const moe_lora_scoring *sc) {
-  if (check_scoring(d, sc) != MOE_LORA_OK || check_groups(d, sc) != MOE_LORA_OK || d->num_tokens == 0) return 0;
+  if (check_scoring(d, sc) != MOE_LORA_OK || check_choice(d, sc) != MOE_LORA_OK || d->num_tokens == 0) return 0;
   return moe::scored_workspace_bytes(d->num_tokens, d->num_experts, d->top_k, sc->n_group > 1,
                                      moe::scored_wide(sc->bias != nullptr, sc->n_group, sc->group_score));
 }
@@ -185,7 +186,7 @@ int moe_lora_route_scored(const moe_lora_dims *d, const moe_lora_scoring *sc, co
                           int32_t *topk_ids, float *topk_weights, int32_t *expert_offsets, int32_t *e2p,
                           int32_t *p2e, void *ws, size_t ws_bytes, moe_lora_stream_t stream) {
   int st = check_scoring(d, sc);
-  if (st != MOE_LORA_OK || (st = check_groups(d, sc)) != MOE_LORA_OK) return st;
+  if (st != MOE_LORA_OK || (st = check_choice(d, sc)) != MOE_LORA_OK) return st;
   if (sc->bias && !aligned16(sc->bias)) return MOE_LORA_ERR_INVALID_ARGUMENT;
   if (!expert_offsets || !aligned16(expert_offsets)) return MOE_LORA_ERR_INVALID_ARGUMENT;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);

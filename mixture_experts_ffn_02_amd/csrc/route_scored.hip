@@ -440,7 +440,7 @@ __global__ __launch_bounds__(256) void scored_backward_kernel(const ScoredBackwa
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, sub = lane / LPT, ll = lane % LPT;
   const int pitch = (E + 3) & ~3;
   float *at = reinterpret_cast<float *>(smem) + (wave * TPW + sub) * pitch;
-  const int t = (blockIdx.x * 4 + wave) * TPW + sub;
+  const long long t = (block_of_grid() * 4 + wave) * TPW + sub;
   const bool tv = t < P.T;
   const size_t row = (size_t)(tv ? t : 0) * E;
   const bool sigmoid = P.score == MOE_LORA_SCORE_SIGMOID;
@@ -633,7 +633,7 @@ int launch_backward(const ScoredBackwardArgs &a, hipStream_t s) {
   const int per_wg = 4 * (64 / LPT);
   const int chunks = (a.E + LPT * VEC - 1) / (LPT * VEC);
   const size_t lds = (size_t)per_wg * ((a.E + 3) & ~3) * sizeof(float);
-  const dim3 grid((a.T + per_wg - 1) / per_wg);
+  const dim3 grid = grid_of_blocks(((long long)a.T + per_wg - 1) / per_wg);
 #define MOE_BWD(CH) scored_backward_kernel<LPT, VEC, CH><<<grid, 256, lds, s>>>(a)
   if (chunks <= 1)
     MOE_BWD(1);
