@@ -443,7 +443,8 @@ int moe_lora_project(const moe_lora_proj_dims *dims, const uint16_t *x, const ui
  * all bf16, sums in fp32 (u enters dx as two bf16 terms, da and db whole), every element
  * written: zeros for adapters without tokens and past an adapter's rank.  Repeated calls
  * give the same bits.  Where the formula meets an infinity, da and db hold an infinity or
- * NaN.  dx, da and db may each be NULL (not wanted; not all three).
+ * NaN.  dx, da and db may each be NULL (not wanted; not all three, unless there are no tokens or
+ * no adapters).
  *   x: the forward's input in bf16 (rows dims->ldx apart), or its 8-bit checkpoint (x_codes,
  *   x_exps, x NULL); for da only.  w: for dx only.  v: the forward's v; for db only.
  * Giving both forms of x, or neither with da, is MOE_LORA_ERR_INVALID_ARGUMENT.

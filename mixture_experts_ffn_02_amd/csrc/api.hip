@@ -508,7 +508,8 @@ int moe_lora_project_backward(const moe_lora_proj_dims *d, const uint16_t *x, co
                               size_t ws_bytes, moe_lora_stream_t stream) {
   const int st = check_proj(d, p, d && d->num_tokens == 0);
   if (st != MOE_LORA_OK) return st;
-  if (!dx && !da && !db) return MOE_LORA_ERR_INVALID_ARGUMENT;
+  // (gradients without elements may come as NULL)
+  if (!dx && !da && !db) return d->num_tokens == 0 || p->num_slots == 0 ? MOE_LORA_OK : MOE_LORA_ERR_INVALID_ARGUMENT;
   if (!aligned16(dx) || !aligned16(da) || !aligned16(db)) return MOE_LORA_ERR_INVALID_ARGUMENT;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   if (d->num_tokens == 0) {  // the adapters' gradients are sums over nothing

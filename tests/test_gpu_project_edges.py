@@ -1,0 +1,29 @@
+"""Calls of the projection with pooled adapters at the edges of what its documentation allows."""
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import dev, f64
+from mixture_experts_ffn_02_amd import moe_lora as ml
+from test_gpu_project import Case
+
+pytestmark = pytest.mark.gpu
+
+
+def test_backward_into_gradients_without_elements():
+    """No tokens: dx has no elements; no adapters: da and db have none.  They may be all that is wanted."""
+    c = Case(8, 64, 48, 2, 16)
+    bf16 = dict(dtype=torch.bfloat16, device=dev())
+    none = c.pool.with_slots(c.pool.token_slot[:0])
+    ml.moe_lora_project_backward(torch.empty((0, 48), **bf16), c.w, none, None, None, dx=torch.empty((0, 64), **bf16))
+    dy = torch.ones((8, 48), **bf16)
+    empty = ml.AdapterPool(c.pool.token_slot, c.pool.rank[:0], c.pool.scaling[:0], c.a[:0], c.b[:0])
+    da, db = torch.empty((0, 16, 64), **bf16), torch.empty((0, 48, 16), **bf16)
+    ml.moe_lora_project_backward(dy, c.w, empty, None, None, x=c.x, da=da, db=db)
+    dx = torch.full((8, 64), float("nan"), **bf16)
+    ml.moe_lora_project_backward(dy, c.w, empty, None, None, x=c.x, dx=dx, da=da, db=db)
+    want = f64(dy) @ f64(c.w)
+    # one rounding to bf16 of a sum of 48 products, each sum step off by 2^-24 of the terms' sizes
+    tol = 2.0 ** -8 * np.abs(want) + 48 * 2.0 ** -24 * np.abs(f64(c.w)).sum(0)
+    assert (np.abs(f64(dx) - want) <= tol).all()

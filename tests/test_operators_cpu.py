@@ -321,3 +321,10 @@ def test_project_gradient_oracle_equals_differences():
             up[i][at] += 1e-6
             down[i][at] -= 1e-6
             assert abs((loss(*up) - loss(*down)) / 2e-6 - got[at]) < 1e-7
+
+
+def test_project_backward_into_gradients_without_elements():
+    none = dict(dx=None, da=None, db=None)
+    assert _back(_lib.ProjDims(0, 64, 48, 64, 48), _pool(), **none) == _lib.OK
+    assert _back(_lib.ProjDims(4, 64, 48, 64, 48), _pool(num_slots=0), **none) == _lib.OK
+    assert _back(_lib.ProjDims(4, 64, 44, 64, 48), _pool(), **none) == _lib.ERR_UNSUPPORTED
