@@ -262,6 +262,12 @@ def _rows_cols(name: str, t: torch.Tensor):
     return t.shape
 
 
+def _int32(what: str, *values: int) -> None:
+    """Refuses what a 32-bit field of the library's structs would cut off."""
+    if max(values) > 0x7FFFFFFF:
+        raise ValueError(f"{what}: {max(values)} does not fit 32 bits")
+
+
 def checkpoint_exps_shape(rows: int, cols: int):
     """Shape of the exponent bytes of a [rows, cols] checkpoint."""
     return rows, (cols + 31) // 32
@@ -270,6 +276,7 @@ def checkpoint_exps_shape(rows: int, cols: int):
 def moe_lora_checkpoint_pack(x, codes, exps, stream=None) -> None:
     """x [rows, cols] bf16 -> codes [rows, cols] and exps [rows, ceil(cols / 32)], uint8."""
     M, H = _rows_cols("x", x)
+    _int32("columns of x", H)
     _call("moe_lora_checkpoint_pack", _on(x, codes, exps), stream, M, H,
           _checked("x", x, torch.bfloat16, M * H), _checked("codes", codes, torch.uint8, M * H),
           _checked("exps", exps, torch.uint8, M * ((H + 31) // 32)))
@@ -277,6 +284,7 @@ def moe_lora_checkpoint_pack(x, codes, exps, stream=None) -> None:
 
 def moe_lora_checkpoint_unpack(codes, exps, x, stream=None) -> None:
     M, H = _rows_cols("codes", codes)
+    _int32("columns of codes", H)
     _call("moe_lora_checkpoint_unpack", _on(codes, exps, x), stream, M, H,
           _checked("codes", codes, torch.uint8, M * H), _checked("exps", exps, torch.uint8, M * ((H + 31) // 32)),
           _checked("x", x, torch.bfloat16, M * H))
@@ -325,6 +333,7 @@ class AdapterPool:
         if self.b.shape != (S, N, R):
             raise ValueError(f"b: [{S}, out, {R}] expected, got shape {tuple(self.b.shape)}")
         bf16 = torch.bfloat16
+        _int32("sizes of the pool", S, R)
         object.__setattr__(self, "_c", _lib.Pool(
             S, R, _checked("token_slot", self.token_slot, torch.int32, T),
             _checked("rank", self.rank, torch.int32, S), _checked("scaling", self.scaling, torch.float32, S),
@@ -372,8 +381,13 @@ def _matrix(name: str, t: torch.Tensor, rows: int, cols: int):
     return t.data_ptr(), pitch if rows > 1 else cols
 
 
+def _proj_dims(T: int, K: int, N: int, ldx: int, ldy: int) -> _lib.ProjDims:
+    _int32("tokens, features, or elements that rows are apart", T, K, N, ldx, ldy)
+    return _lib.ProjDims(T, K, N, ldx, ldy)
+
+
 def moe_lora_project_workspace_size(T: int, K: int, N: int, pool: AdapterPool) -> int:
-    return int(load().moe_lora_project_workspace_size(ctypes.byref(_lib.ProjDims(T, K, N, K, N)),
+    return int(load().moe_lora_project_workspace_size(ctypes.byref(_proj_dims(T, K, N, K, N)),
                                                       ctypes.byref(pool.to_c(T, K, N))))
 
 
@@ -386,13 +400,13 @@ def moe_lora_project(x, w, pool: AdapterPool, y, ws, v=None, stream=None) -> Non
     px, ldx = _matrix("x", x, T, K)
     py, ldy = _matrix("y", y, T, N)
     _call("moe_lora_project", pool.on(_on(x, w, y, ws, v)), stream,
-          ctypes.byref(_lib.ProjDims(T, K, N, ldx, ldy)), px, _checked("w", w, torch.bfloat16, N * K),
+          ctypes.byref(_proj_dims(T, K, N, ldx, ldy)), px, _checked("w", w, torch.bfloat16, N * K),
           ctypes.byref(p), py, None if v is None else _checked("v", v, torch.float32, T * p.max_rank),
           *_workspace(ws))
 
 
 def moe_lora_project_backward_workspace_size(T: int, K: int, N: int, pool: AdapterPool) -> int:
-    return int(load().moe_lora_project_backward_workspace_size(ctypes.byref(_lib.ProjDims(T, K, N, K, N)),
+    return int(load().moe_lora_project_backward_workspace_size(ctypes.byref(_proj_dims(T, K, N, K, N)),
                                                                ctypes.byref(pool.to_c(T, K, N))))
 
 
@@ -408,7 +422,8 @@ def moe_lora_project_backward(dy, w, pool: AdapterPool, v, ws, x=None, x_codes=N
     px, ldx = (None, K) if x is None else _matrix("x", x, T, K)
     pdy, ldy = _matrix("dy", dy, T, N)
     _call("moe_lora_project_backward",
-          pool.on(_on(dy, w, v, ws, x, x_codes, x_exps, dx, da, db)), stream, ctypes.byref(_lib.ProjDims(T, K, N, ldx, ldy)), px,
+          pool.on(_on(dy, w, v, ws, x, x_codes, x_exps, dx, da, db)), stream,
+          ctypes.byref(_proj_dims(T, K, N, ldx, ldy)), px,
           None if x_codes is None else _checked("x_codes", x_codes, u8, T * K),
           None if x_exps is None else _checked("x_exps", x_exps, u8, T * ((K + 31) // 32)),
           _checked("w", w, bf16, N * K), ctypes.byref(p),

@@ -27,3 +27,20 @@ def test_backward_into_gradients_without_elements():
     # one rounding to bf16 of a sum of 48 products, each sum step off by 2^-24 of the terms' sizes
     tol = 2.0 ** -8 * np.abs(want) + 48 * 2.0 ** -24 * np.abs(f64(c.w)).sum(0)
     assert (np.abs(f64(dx) - want) <= tol).all()
+
+
+def test_rows_farther_apart_than_an_int_holds():
+    """A pitch of 2^32 + 64 elements: refused, and not taken as 64."""
+    far = 2 ** 32 + 64
+    c = Case(2, 64, 48, 2, 16)
+    ws = torch.empty((1 << 16,), dtype=torch.uint8, device=dev())
+    wide = torch.zeros((far + 64,), dtype=torch.bfloat16, device=dev())
+    x, y = wide.as_strided((2, 64), (far, 1)), torch.full((2, 48), 7.0, dtype=torch.bfloat16, device=dev())
+    with pytest.raises(ValueError, match="32 bits"):
+        ml.moe_lora_project(x, c.w, c.pool, y, ws)
+    with pytest.raises(ValueError, match="32 bits"):
+        ml.moe_lora_project(c.x, c.w, c.pool, wide.as_strided((2, 48), (far, 1)), ws)
+    with pytest.raises(ValueError, match="32 bits"):
+        ml.moe_lora_project_backward(wide.as_strided((2, 48), (far, 1)), c.w, c.pool, None, ws, dx=torch.empty_like(c.x))
+    torch.cuda.synchronize()
+    assert (y == 7.0).all() and (wide == 0).all()

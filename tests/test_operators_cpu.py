@@ -328,3 +328,22 @@ def test_project_backward_into_gradients_without_elements():
     assert _back(_lib.ProjDims(0, 64, 48, 64, 48), _pool(), **none) == _lib.OK
     assert _back(_lib.ProjDims(4, 64, 48, 64, 48), _pool(num_slots=0), **none) == _lib.OK
     assert _back(_lib.ProjDims(4, 64, 44, 64, 48), _pool(), **none) == _lib.ERR_UNSUPPORTED
+
+
+def test_binding_refuses_what_32_bits_cut_off():
+    for at in range(5):
+        sizes = [8] * 5
+        sizes[at] = 2 ** 32 + 8
+        with pytest.raises(ValueError, match="32 bits"):
+            ml._proj_dims(*sizes)
+    assert ml._proj_dims(4, 8, 16, 8, 2 ** 31 - 1).ldy == 2 ** 31 - 1  # (the library's own limits come next)
+    wide = torch.empty((1, 2 ** 32 + 8), dtype=torch.uint8, device="meta")
+    with pytest.raises(ValueError, match="columns"):
+        ml.moe_lora_checkpoint_pack(wide, wide, wide)
+    with pytest.raises(ValueError, match="columns"):
+        ml.moe_lora_checkpoint_unpack(wide, wide, wide)
+    meta = dict(dtype=torch.bfloat16, device="meta")
+    with pytest.raises(ValueError, match="pool"):
+        ml.AdapterPool(torch.empty(1, dtype=torch.int32, device="meta"), torch.empty(1, dtype=torch.int32, device="meta"),
+                       torch.empty(1, device="meta"), torch.empty((1, 2 ** 32 + 8, 8), **meta),
+                       torch.empty((1, 8, 2 ** 32 + 8), **meta))
