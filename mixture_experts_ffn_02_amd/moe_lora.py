@@ -504,13 +504,18 @@ class MoELoRALayer:
     def dims(self, T: int) -> Dims:
         return Dims(T, self.H, self.I, self.E, self.k)
 
+    def _route_form(self):
+        """What the routing workspace depends on beside the batch (a Scoring may change between calls)."""
+        r = self.routing
+        return (r.bias is not None, r.n_group > 1, r.group_score) if isinstance(r, Scoring) else None
+
     def _route_workspace(self, d: Dims) -> int:
         if isinstance(self.routing, Scoring):
             return moe_lora_route_scored_workspace_size(d, self.routing)
         return moe_lora_route_workspace_size(d)
 
     def _buffers(self, T: int, lora: Optional[Adapters], device) -> dict:
-        key = (T, None if lora is None else tuple(lora.rank[: lora.num_slots]))
+        key = (T, None if lora is None else tuple(lora.rank[: lora.num_slots]), self._route_form())
         b = self._bufs.get(key)
         if b is None:
             d = self.dims(T)
