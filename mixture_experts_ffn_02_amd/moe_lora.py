@@ -500,6 +500,7 @@ class MoELoRALayer:
                                    _ptr(correction_bias) if correction_bias is not None else None)
         self.gather_on_load = gather_on_load
         self._bufs = {}
+        self._used = {}  # (tokens, ranks) -> the buffers of the last call with them
 
     def dims(self, T: int) -> Dims:
         return Dims(T, self.H, self.I, self.E, self.k)
@@ -537,6 +538,13 @@ class MoELoRALayer:
                 "out": torch.empty((T, self.H), dtype=torch.bfloat16, device=device),
             }
             self._bufs[key] = b
+        self._used[key[:2]] = b
+        return b
+
+    def _last(self, T: int, lora: Optional[LoRASlots]) -> dict:
+        b = self._used.get((T, None if lora is None else tuple(lora.to_c().rank[: len(lora.rank)])))
+        if b is None:
+            raise ValueError(f"the layer has not run a batch of {T} tokens with these adapters")
         return b
 
     def __call__(self, x: torch.Tensor, logits: torch.Tensor, lora: Optional[LoRASlots] = None,
@@ -571,5 +579,6 @@ class MoELoRALayer:
         return b["out"]
 
     def last_route(self, T: int, lora: Optional[LoRASlots] = None) -> RouteOut:
-        b = self._buffers(T, lora.to_c() if lora is not None else None, None)
+        """Routing outputs of the last call with T tokens and these adapters' ranks."""
+        b = self._last(T, lora)
         return RouteOut(b["ids"], b["w"], b["off"], b["e2p"], b["p2e"])

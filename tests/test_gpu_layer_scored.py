@@ -33,3 +33,19 @@ def test_the_scoring_changes_between_two_calls(change):
     layer(g.x, g.logits)
     torch.cuda.synchronize()
     assert torch.equal(layer.last_route(40).topk_ids, first)
+
+
+def test_last_route_before_a_call():
+    """Nothing to give, and nothing is left behind for the call that follows."""
+    g = GpuLayer(Workload(make_config(T=40, H=64, I=32, E=32, top_k=4)))
+    layer = ml.MoELoRALayer(64, 32, 32, 4, g.w1, g.w2, ml.Scoring("sigmoid", True))
+    with pytest.raises(ValueError, match="has not run"):
+        layer.last_route(40)
+    layer(g.x, g.logits)
+    assert layer.last_route(40).topk_ids.is_cuda
+    layer.routing.bias = torch.zeros(32, device=dev())
+    assert layer.last_route(40).topk_ids.is_cuda
+    layer(g.x, g.logits)
+    torch.cuda.synchronize()
+    assert np.array_equal(layer.last_route(40).topk_ids.cpu().numpy(),
+                          ref.route_scored(f64(g.logits), 4, "sigmoid", bias=np.zeros(32))[0])

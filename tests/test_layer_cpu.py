@@ -1,0 +1,20 @@
+"""MoELoRALayer's bookkeeping on the CPU (no call reaches the library's kernels)."""
+
+import pytest
+import torch
+
+from mixture_experts_ffn_02_amd import moe_lora as ml
+
+
+def make_layer(routing=ml.ROUTING_RENORMALIZE):
+    w1, w2 = torch.zeros((4, 32, 8), dtype=torch.bfloat16), torch.zeros((4, 8, 16), dtype=torch.bfloat16)
+    return ml.MoELoRALayer(8, 16, 4, 2, w1, w2, routing)
+
+
+@pytest.mark.parametrize("routing", [ml.ROUTING_RENORMALIZE, ml.Scoring()], ids=["named", "scored"])
+def test_last_route_before_a_call_leaves_no_buffers_behind(routing):
+    """They would be on the host, and the next call of that size would hand them to the GPU."""
+    layer = make_layer(routing)
+    with pytest.raises(ValueError, match="has not run"):
+        layer.last_route(40)
+    assert not layer._bufs
