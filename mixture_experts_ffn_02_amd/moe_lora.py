@@ -582,3 +582,8 @@ class MoELoRALayer:
         """Routing outputs of the last call with T tokens and these adapters' ranks."""
         b = self._last(T, lora)
         return RouteOut(b["ids"], b["w"], b["off"], b["e2p"], b["p2e"])
+
+    def last_rows(self, T: int, lora: Optional[LoRASlots] = None) -> torch.Tensor:
+        """The routed rows [T * k, H] that the last such call summed (moe_lora_finalize_backward
+        takes them).  The layer's own buffer: the next call of that size writes it again."""
+        return self._last(T, lora)["y"]

@@ -49,3 +49,21 @@ def test_last_route_before_a_call():
     torch.cuda.synchronize()
     assert np.array_equal(layer.last_route(40).topk_ids.cpu().numpy(),
                           ref.route_scored(f64(g.logits), 4, "sigmoid", bias=np.zeros(32))[0])
+
+
+def test_the_routed_rows_of_the_last_call():
+    """last_rows holds what finalize summed: finalize over them gives the output again, and they feed its gradients."""
+    g = GpuLayer(Workload(make_config(T=40, H=64, I=32, E=32, top_k=4)))
+    layer = ml.MoELoRALayer(64, 32, 32, 4, g.w1, g.w2, ml.Scoring("softmax", False))
+    out = layer(g.x, g.logits)
+    rows, rt, d = layer.last_rows(40), layer.last_route(40), layer.dims(40)
+    assert rows.shape == (160, 64) and rows.dtype == torch.bfloat16
+    again = torch.empty_like(out)
+    ml.moe_lora_finalize(d, rows, rt.topk_weights, rt.e2p, again)
+    assert torch.equal(again, out)
+    d_out = torch.randn((40, 64), device=dev()).to(torch.bfloat16)
+    d_rows, d_w = torch.empty_like(rows), torch.empty((40, 4), device=dev())
+    ml.moe_lora_finalize_backward(d, d_out, rt.topk_weights, rt.e2p, d_rows, d_w, y_perm=rows)
+    want = ref.finalize_backward(f64(d_out), f64(rows), rt.topk_weights.double().cpu().numpy(), rt.e2p.cpu().numpy())[1]
+    size = np.abs(f64(d_out)).max() * np.abs(f64(rows)).max() * 64
+    np.testing.assert_allclose(d_w.double().cpu().numpy(), want, rtol=0, atol=2 * 64 * 2.0 ** -24 * size)

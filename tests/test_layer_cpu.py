@@ -18,3 +18,8 @@ def test_last_route_before_a_call_leaves_no_buffers_behind(routing):
     with pytest.raises(ValueError, match="has not run"):
         layer.last_route(40)
     assert not layer._bufs
+
+
+def test_last_rows_before_a_call():
+    with pytest.raises(ValueError, match="has not run"):
+        make_layer().last_rows(40)
