@@ -8,6 +8,7 @@ kernels of libmoe_lora.so.  Tensors are passed by data pointer: bf16 tensors may
 from __future__ import annotations
 
 import ctypes
+from contextlib import nullcontext
 from dataclasses import dataclass, field
 from typing import Optional, Sequence
 
@@ -434,6 +435,12 @@ def moe_lora_project_backward(dy, w, pool: AdapterPool, v, ws, x=None, x_codes=N
           *_workspace(ws))
 
 
+def _device_of(t: torch.Tensor):
+    """A context in which t's device is the current one."""
+    dev = t.get_device()
+    return nullcontext() if dev < 0 or dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)
+
+
 @dataclass
 class RouteOut:
     topk_ids: torch.Tensor
@@ -483,8 +490,9 @@ class MoELoRALayer:
             w1p = torch.empty_like(w_gate_up) if to_pack & PACKED_GATE_UP else None
             w2p = torch.empty_like(w_down) if to_pack & PACKED_DOWN else None
             pack = moe_lora_pack_weights_fp8 if self.w_scales is not None else moe_lora_pack_weights
-            pack(self.dims(0), w_gate_up if w1p is not None else None, w_down if w2p is not None else None,
-                 w1p, w2p)
+            with _device_of(w_gate_up):
+                pack(self.dims(0), w_gate_up if w1p is not None else None, w_down if w2p is not None else None,
+                     w1p, w2p)
             w_gate_up = w1p if w1p is not None else w_gate_up
             w_down = w2p if w2p is not None else w_down
         self.packed_weights = to_pack | pre
@@ -549,6 +557,10 @@ class MoELoRALayer:
 
     def __call__(self, x: torch.Tensor, logits: torch.Tensor, lora: Optional[LoRASlots] = None,
                  side_stream=None, opts: Optional[Options] = None, stream=None) -> torch.Tensor:
+        with _device_of(x):  # every launch of the call on x's device, and on its stream where none is given
+            return self._run(x, logits, lora, side_stream, opts, stream)
+
+    def _run(self, x, logits, lora, side_stream, opts, stream) -> torch.Tensor:
         T = x.shape[0]
         c_lora = lora.to_c() if lora is not None else None
         b = self._buffers(T, c_lora, x.device)

@@ -1,5 +1,8 @@
 """MoELoRALayer's bookkeeping on the CPU (no call reaches the library's kernels)."""
 
+import contextlib
+from types import SimpleNamespace
+
 import pytest
 import torch
 
@@ -23,3 +26,29 @@ def test_last_route_before_a_call_leaves_no_buffers_behind(routing):
 def test_last_rows_before_a_call():
     with pytest.raises(ValueError, match="has not run"):
         make_layer().last_rows(40)
+
+
+@pytest.mark.parametrize("current,used", [(0, [1]), (1, [])])
+@pytest.mark.parametrize("routing", [ml.ROUTING_RENORMALIZE, ml.Scoring()], ids=["named", "scored"])
+def test_every_launch_of_a_call_is_on_the_inputs_device(monkeypatch, routing, current, used):
+    """With a Scoring, routing ran on the tensors' device and the rest of the layer on the current one, on a stream
+    that nothing orders behind it."""
+    at, entered, launches = [current], [], []
+
+    @contextlib.contextmanager
+    def device(dev):
+        entered.append(dev)
+        before, at[0] = at[0], dev
+        yield
+        at[0] = before
+
+    layer = make_layer(routing)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: at[0])
+    monkeypatch.setattr(torch.cuda, "device", device)
+    for name in ("route", "route_scored", "forward", "finalize"):
+        monkeypatch.setattr(ml, "moe_lora_" + name, lambda *a, name=name, **k: launches.append((name, at[0])))
+    x = SimpleNamespace(shape=(3, 8), device="cpu", get_device=lambda: 1)
+    layer(x, None)
+    first = "route_scored" if isinstance(routing, ml.Scoring) else "route"
+    assert launches == [(first, 1), ("forward", 1), ("finalize", 1)]
+    assert entered == used and at[0] == current
