@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 from contextlib import nullcontext
-from dataclasses import dataclass, field
+from dataclasses import dataclass, field, fields
 from typing import Optional, Sequence
 
 import torch
@@ -216,6 +216,13 @@ class Scoring:
     scale: float = 1.0
     bias: Optional[torch.Tensor] = None
 
+    def __eq__(self, other):
+        """The same method with the same bias tensor (whose values are not compared)."""
+        if not isinstance(other, Scoring):
+            return NotImplemented
+        return all(getattr(self, f.name) == getattr(other, f.name) for f in fields(self) if f.name != "bias") and \
+            self.bias is other.bias
+
     def to_c(self, logits_dtype: torch.dtype, num_experts: int) -> _lib.ScoringC:
         if self.score not in ("softmax", "sigmoid"):
             raise ValueError(f"score: 'softmax' or 'sigmoid', got {self.score!r}")
@@ -306,7 +313,7 @@ def moe_lora_finalize_backward(d: Dims, d_out, topk_weights, e2p, d_y_perm, d_we
           _checked("d_weights", d_weights, torch.float32, R))
 
 
-@dataclass(frozen=True)
+@dataclass(frozen=True, eq=False)  # (a pool equals itself: comparing tensors gives no truth value)
 class AdapterPool:
     """Resident adapters of a projection (device tensors): a [S, R, in] and b [S, out, R] bf16,
     rank [S] int32 and scaling [S] fp32; token_slot [T] int32 names each token's adapter

@@ -347,3 +347,14 @@ def test_binding_refuses_what_32_bits_cut_off():
         ml.AdapterPool(torch.empty(1, dtype=torch.int32, device="meta"), torch.empty(1, dtype=torch.int32, device="meta"),
                        torch.empty(1, device="meta"), torch.empty((1, 2 ** 32 + 8, 8), **meta),
                        torch.empty((1, 8, 2 ** 32 + 8), **meta))
+
+
+def test_descriptors_that_hold_tensors_compare():
+    i32, bf16 = torch.int32, torch.bfloat16
+    pools = [ml.AdapterPool(torch.zeros(5, dtype=i32), torch.ones(2, dtype=i32), torch.ones(2),
+                            torch.zeros((2, 8, 16), dtype=bf16), torch.zeros((2, 24, 8), dtype=bf16)) for _ in range(2)]
+    assert pools[0] == pools[0] and pools[0] != pools[1] and len(set(pools)) == 2
+    bias = torch.zeros(8)
+    assert ml.Scoring(bias=bias) == ml.Scoring(bias=bias) and ml.Scoring() == ml.Scoring()
+    assert ml.Scoring(bias=bias) != ml.Scoring(bias=bias.clone()) and ml.Scoring(bias=bias) != ml.Scoring()
+    assert ml.Scoring(scale=2.0) != ml.Scoring() and ml.Scoring() != ml.ROUTING_RENORMALIZE
