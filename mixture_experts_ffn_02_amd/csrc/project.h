@@ -42,17 +42,19 @@ MOE_DEV void dma16(const void *base, uint32_t off, uint32_t lds) {
       : "memory");
 }
 // The same, to lds + LDS, where on is not 0 and nothing where it is (wave-uniform), without a
-// branch.  For code that all 64 lanes run: the mask is set back to all of them.  (M0 is
-// reserved: the compiler keeps nothing in it.)
+// branch.  For code that all 64 lanes run: the mask is set back to all of them.
 template <int LDS>
 MOE_DEV void dma16_if(int on, const void *base, uint32_t off, uint32_t lds) {
+  uint32_t saved;
   asm volatile(
-      "s_add_u32 m0, %2, %4\n\t"
-      "s_cmp_lg_u32 %3, 0\n\t"
+      "s_mov_b32 %0, m0\n\t"
+      "s_add_u32 m0, %3, %5\n\t"
+      "s_cmp_lg_u32 %4, 0\n\t"
       "s_cselect_b64 exec, -1, 0\n\t"
-      "global_load_lds_dwordx4 %0, %1\n\t"
-      "s_mov_b64 exec, -1"
-      :
+      "global_load_lds_dwordx4 %1, %2\n\t"
+      "s_mov_b64 exec, -1\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
       : "v"(off), "s"(base), "s"(lds), "s"(on), "n"(LDS)
       : "memory", "scc");
 }
