@@ -188,10 +188,13 @@ int moe_lora_route(const moe_lora_dims *dims, int routing, const moe_lora_groupe
  *   the top_k keys among the kept groups are chosen (ties -> lower expert index);
  *   weight = scale * p, or scale * p / (sum of the chosen p) with renormalize.
  * Keys with a bias, and groups scored by two, are compared in fp64; weights are fp32.
- * A logit of -inf masks its expert: it is chosen only where fewer than top_k others are
- * left, with weight 0; a token whose experts are all masked has weights 0.  A NaN counts as
- * the largest key, and its token's weights follow the formula; ids are always distinct and
- * in range.
+ * A logit of -inf masks its expert: p and weight are 0.  The choice still goes by the keys:
+ *   without a bias and groups it is taken only where fewer than top_k others are left;
+ *   with a bias its key is the bias alone, which precedes a live expert of a smaller key (a
+ *     bias of -inf as well keeps it behind all that are live);
+ *   with groups it precedes, in a kept group, every expert of a closed one.
+ * A token whose experts are all masked has weights 0.  A NaN counts as the largest key, and its
+ * token's weights follow the formula; ids are always distinct and in range.
  * Limits: num_tokens <= 65536 (MOE_LORA_ERR_UNSUPPORTED; route larger batches in chunks).
  * dims: num_tokens, num_experts and top_k are used (hidden and inter only checked).
  * Workspace: moe_lora_route_scored_workspace_size bytes (0 where the batch takes one launch:

@@ -31,3 +31,31 @@ def test_gradient_of_a_batch_longer_than_a_forward_call(E, k):
     want = ref.route_scored_backward(l, ids, dw.astype(np.float64), "softmax", False)
     np.testing.assert_allclose(out[:some].double().cpu().numpy(), want, rtol=2.0 ** -24 + REL,
                                atol=REL * np.abs(dw).max() * k)
+
+
+@pytest.mark.parametrize("score,renorm", list(itertools.product(["softmax", "sigmoid"], [True, False])))
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("T", [12, 300])
+def test_masked_experts_beside_a_bias_and_groups(T, sign, score, renorm):
+    """A masked expert competes with its bias alone as its key, weighs 0 if it is chosen, and stays out where its bias
+    is -inf too; in groups without a bias it goes before the experts of closed groups."""
+    E, k = 32, 6
+    t, _ = make_logits(T, E, "f32", 43, masked=12)
+    l = t.double().numpy()
+    off = np.isinf(l[0])
+    bias = (sign * np.random.Generator(np.random.PCG64(3)).random(E) * 0.3).astype(np.float32)
+    for kw in ({}, dict(n_group=4, topk_group=2, group_score=1), dict(n_group=8, topk_group=3, group_score=2)):
+        check_route(t, l, k, scoring(score, renorm, bias, **kw), bias)
+        ids, w, *_ = run_route(t, k, scoring(score, renorm, bias, **kw))
+        assert (w[off[ids]] == 0).all()
+        check_route(t, l, k, scoring(score, renorm, **kw))
+    # the smallest case of the documentation: expert 0 is masked, and its bias is the largest key but one
+    t4 = torch.tensor([[-np.inf, 0.0, 0.1, 0.2]] * T)
+    b4 = np.float32([0.3, -0.6, -0.6, 0.0])
+    ids, w, *_ = run_route(t4, 2, scoring("sigmoid", renorm, b4))
+    assert (ids == [3, 0]).all() and (w[:, 1] == 0).all()
+    never = bias.copy()
+    never[off] = -np.inf
+    for kw in ({}, dict(n_group=4, topk_group=4, group_score=1)):
+        check_route(t, l, k, scoring(score, renorm, never, **kw), never)
+        assert not off[run_route(t, k, scoring(score, renorm, never, **kw))[0]].any()

@@ -144,6 +144,20 @@ def test_scored_oracle_holds_the_named_methods():
     np.testing.assert_allclose(got_w, w, rtol=1e-12)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_masked_experts_in_the_choice(score):
+    l = np.array([[-np.inf, 0.0, 0.1, 0.2]])
+    assert list(ref.route_scored(l, 3, score)[0][0]) == [3, 2, 1]
+    ids, w = ref.route_scored(l, 2, score, bias=np.float32([0.3, -0.6, -0.6, 0.0]))
+    assert sorted(ids[0]) == [0, 3] and (w[ids == 0] == 0).all()  # its bias alone is its key
+    ids, w = ref.route_scored(l, 3, score, bias=np.float32([-np.inf, -0.6, -0.6, 0.0]))
+    assert 0 not in ids[0]
+    ids, w = ref.route_scored(l[:, ::-1], 2, score, n_group=2, topk_group=1)
+    assert list(ids[0]) == [0, 1]                                 # groups [0.2, 0.1] and [0.0, masked]
+    ids, w = ref.route_scored(np.array([[9.0, -np.inf, 1.0, 2.0]]), 2, score, n_group=2, topk_group=1)
+    assert list(ids[0]) == [0, 1] and w[0, 1] == 0                # before the closed group's experts
+
+
 @pytest.mark.parametrize("score,renorm", list(itertools.product(["softmax", "sigmoid"], [True, False])))
 def test_scored_gradient_equals_differences(score, renorm):
     l = _logits(3, 7, 2)
