@@ -44,3 +44,28 @@ def test_rows_farther_apart_than_an_int_holds():
         ml.moe_lora_project_backward(wide.as_strided((2, 48), (far, 1)), c.w, c.pool, None, ws, dx=torch.empty_like(c.x))
     torch.cuda.synchronize()
     assert (y == 7.0).all() and (wide == 0).all()
+
+
+def test_other_streams():
+    """Inputs made on one stream, calls on others behind it: each gets the result of the first call."""
+    c = Case(500, 512, 776, 6, 32)
+    y, v = c.forward()
+    want = {k: t.clone() for k, t in c.backward().items()}
+    dy, v_in = c.dy, c.v
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    for st in (side, other):
+        st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):  # the current stream, buffers and fills included
+        y2, v2 = c.forward()
+    y3, v3 = torch.zeros_like(y), torch.zeros_like(v)
+    got = {k: torch.zeros_like(t) for k, t in want.items()}
+    ws = torch.empty((ml.moe_lora_project_workspace_size(500, 512, 776, c.pool),), dtype=torch.uint8, device=dev())
+    ws_b = torch.empty((ml.moe_lora_project_backward_workspace_size(500, 512, 776, c.pool),), dtype=torch.uint8,
+                       device=dev())
+    for st in (side, other):
+        st.wait_stream(torch.cuda.current_stream())
+    ml.moe_lora_project(c.x, c.w, c.pool, y3, ws, v=v3, stream=other)
+    ml.moe_lora_project_backward(dy, c.w, c.pool, v_in, ws_b, x=c.x, **got, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(y, y2) and torch.equal(v, v2) and torch.equal(y, y3) and torch.equal(v, v3)
+    assert all(torch.equal(want[k], got[k]) for k in want)

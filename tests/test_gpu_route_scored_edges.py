@@ -59,3 +59,34 @@ def test_masked_experts_beside_a_bias_and_groups(T, sign, score, renorm):
     for kw in ({}, dict(n_group=4, topk_group=4, group_score=1)):
         check_route(t, l, k, scoring(score, renorm, never, **kw), never)
         assert not off[run_route(t, k, scoring(score, renorm, never, **kw))[0]].any()
+
+
+@pytest.mark.parametrize("with_bias", [False, True], ids=["logits", "bias"])
+@pytest.mark.parametrize("score,renorm,dtype", [("softmax", False, "f32"), ("softmax", True, "bf16"),
+                                                ("sigmoid", True, "f32")])
+@pytest.mark.parametrize("E,k", [(130, 4), (200, 8), (256, 16), (384, 8), (509, 3), (512, 16)])
+def test_many_experts_in_a_long_batch(E, k, score, renorm, dtype, with_bias):
+    """More than 4096 tokens: 16 lanes to a token, 16 or 32 experts in each."""
+    T = 4100
+    say(f"[scored 16 lanes] E={E} k={k} {score} {renorm} {dtype} bias={with_bias}")
+    t, l = make_logits(T, E, dtype, 44, ties=dtype == "f32" and E % 2 == 0)
+    bias = np.random.Generator(np.random.PCG64(6)).standard_normal(E).astype(np.float32) * 0.1 if with_bias else None
+    check_route(t, l, k, scoring(score, renorm, bias, scale=1.5), bias)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [24, 64, 130, 384, 512])
+def test_near_ties_in_a_long_batch(E, score):
+    """Biases that bring the keys of neighbours as near as fp32 biases of this size can (at most 2^-24 apart, in either
+    order): below the error of the fp32 keys, so that every token's choice is made again on fp64 keys."""
+    T, k = 4100, 8
+    t, _ = make_logits(T, E, "f32", 45)
+    t[1:] = t[0]
+    t[1::2] = t[0].flip(0)
+    l = t.double().numpy()
+    for row in (0, 1):
+        p = 1 / (1 + np.exp(-l[row])) if score == "sigmoid" else np.exp(l[row] - l[row].max())
+        if score == "softmax":
+            p /= p.sum()
+        bias = (np.linspace(0.9, 0.5, E // 2).repeat(2) - p).astype(np.float32)
+        check_route(t, l, k, scoring(score, True, bias), bias)
