@@ -23,15 +23,15 @@ namespace {
 // out[t, r] = sum_k x[t, k] m[slot][...] over a 16-token tile, for its j-th, (j + J)-th ...
 // distinct adapter.  TR = 0: m is A [S, R, K] (k contiguous); TR = 1: m is B [S, K, R] (r
 // contiguous: read back transposed from LDS).  Stores the terms of s * out, and fp32 out
-// (scaled if TR) where wanted, zeros past the rank.  Each wavefront takes a run of 64-wide K steps, G
-// of them in flight, loaded with neighbouring lanes on neighbouring bytes and turned into
-// MFMA operands through LDS of its own.
+// (scaled if TR) where wanted, zeros past the rank.  Each wavefront takes a run of 64-wide K
+// steps, G of them in flight, loaded with neighbouring lanes on neighbouring bytes and turned
+// into MFMA operands through LDS of its own.
 constexpr int kShrinkWaves = 8;
 
-template <int RT, int MT, bool TR, bool LONG>
-__global__ __launch_bounds__(kShrinkWaves * 64, LONG && MT == 1 ? 3 : 2) void shrink_kernel(const ShrinkArgs P) {
+template <int RT, int MT, bool TR>
+__global__ __launch_bounds__(kShrinkWaves * 64, 2) void shrink_kernel(const ShrinkArgs P) {
   constexpr int RP = RT * 16 + 1;
-  constexpr int G = LONG ? (RT <= 2 ? 2 : 1) : RT <= 2 ? 4 : 2;
+  constexpr int G = (RT <= 2 ? 4 : 2) / MT;
   constexpr int ROWS = 16 * MT, XI = 2 * MT;
   constexpr int kStage = kShrinkWaves * (ROWS + RT * 16) * 64 * 2, kPart = kShrinkWaves * ROWS * RP * 4;
   __shared__ __attribute__((aligned(16))) unsigned char smem[kStage > kPart ? kStage : kPart];
@@ -712,80 +712,80 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
       if (!packed) expand(2 * g + 1, (at + 1) & (NB - 1), left);
     }
   } else {
-  dma_wait_all();
-  __syncthreads();
-  issue(1, 1);
-  u32x4_t af0[FM], bf0[FN];
-#pragma unroll
-  for (int c = 0; c < kReads; ++c) read(0, 0, c, af0, bf0);
-
-  // the g-th of SEG shares of a full step's DMA loads
-  auto dma_one = [&](auto dc, int dbuf, const uint16_t *ab, const uint16_t *bb, int live) MOE_INLINE {
-    constexpr int d = decltype(dc)::value;
-    if constexpr (d < A_IT)
-      dma16_if<d * NT * 16>(live, ab, a_off[d], a_lds(dbuf));
-    else
-      dma16_if<(d - A_IT) * NT * 16>(live, bb, b_off[d - A_IT], b_lds(dbuf));
-  };
-  // products of one half among the reads of (buf, kk); with dma, also among the DMA loads at
-  // k0 into dbuf
-  auto half = [&](u32x4_t(&af)[FM], u32x4_t(&bf)[FN], int buf, int kk, u32x4_t(&an)[FM], u32x4_t(&bn)[FN], auto dma,
-                  int dbuf, int k0, int live) MOE_INLINE {
-    constexpr bool kDma = decltype(dma)::value;
-    constexpr int SEG = kDma ? 8 : 1;  // pieces that the scheduler keeps in order
-    const uint16_t *ab = a_base + k0;
-    const uint16_t *bb = NN ? b_base + (size_t)k0 * N : b_base + k0;
-    __builtin_amdgcn_sched_barrier(0);
-    static_for<0, SEG>([&](auto gc) MOE_INLINE {
-      constexpr int g = decltype(gc)::value;
-      if constexpr (kDma)
-        static_for<g * (A_IT + B_IT) / SEG, (g + 1) * (A_IT + B_IT) / SEG>(
-            [&](auto dc) MOE_INLINE { dma_one(dc, dbuf, ab, bb, live); });
-#pragma unroll
-      for (int c = g * kReads / SEG; c < (g + 1) * kReads / SEG; ++c) read(buf, kk, c, an, bn);
-#pragma unroll
-      for (int m = g * FM * FN / SEG; m < (g + 1) * FM * FN / SEG; ++m)
-        acc[m / FN][m % FN] = mfma_16x16x32(bf[m % FN], af[m / FN], acc[m / FN][m % FN]);
-#pragma unroll
-      for (int c = 0; c < kReads / SEG; ++c) {  // an LDS read, then a share of the products
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, FM * FN / kReads, 0);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    });
-  };
-  // (two steps to an iteration and the branches of issue() between the halves: with both
-  // halves in one basic block, or one step to an iteration, the register allocator moved
-  // accumulators about on every step)
-  auto main_step = [&](int buf, int s) MOE_INLINE {
-    half(af0, bf0, buf, 1, af1, bf1, std::false_type{}, 0, 0, 0);
     dma_wait_all();
     __syncthreads();
-    int left = s + 2 - full;
-    asm volatile("" : "+v"(left));
-    const int more = (int)((uint32_t)__builtin_amdgcn_readfirstlane(left) >> 31);
-    if (!more) issue(buf, s + 2);
-    // (past the last step the reads bring what nothing uses)
-    half(af1, bf1, buf ^ 1, 0, af0, bf0, std::true_type{}, buf, more * (s + 2) * 64, more);
-  };
-#pragma unroll 1
-  for (int s = 0; s < steps; s += 2) {
-    main_step(0, s);
-    if (s + 1 < steps) main_step(1, s + 1);
-  }
+    issue(1, 1);
+    u32x4_t af0[FM], bf0[FN];
+#pragma unroll
+    for (int c = 0; c < kReads; ++c) read(0, 0, c, af0, bf0);
 
-#pragma unroll 1
-  for (int h = 0; h < exts; ++h) {
-    const int buf = (steps + h) & 1;
-    int left;
-    prepare_ext(h, left);
-    expand(h, buf, left);
-    if (h + 1 < exts) {
+    // the g-th of SEG shares of a full step's DMA loads
+    auto dma_one = [&](auto dc, int dbuf, const uint16_t *ab, const uint16_t *bb, int live) MOE_INLINE {
+      constexpr int d = decltype(dc)::value;
+      if constexpr (d < A_IT)
+        dma16_if<d * NT * 16>(live, ab, a_off[d], a_lds(dbuf));
+      else
+        dma16_if<(d - A_IT) * NT * 16>(live, bb, b_off[d - A_IT], b_lds(dbuf));
+    };
+    // products of one half among the reads of (buf, kk); with dma, also among the DMA loads at
+    // k0 into dbuf
+    auto half = [&](u32x4_t(&af)[FM], u32x4_t(&bf)[FN], int buf, int kk, u32x4_t(&an)[FM], u32x4_t(&bn)[FN], auto dma,
+                    int dbuf, int k0, int live) MOE_INLINE {
+      constexpr bool kDma = decltype(dma)::value;
+      constexpr int SEG = kDma ? 8 : 1;  // pieces that the scheduler keeps in order
+      const uint16_t *ab = a_base + k0;
+      const uint16_t *bb = NN ? b_base + (size_t)k0 * N : b_base + k0;
+      __builtin_amdgcn_sched_barrier(0);
+      static_for<0, SEG>([&](auto gc) MOE_INLINE {
+        constexpr int g = decltype(gc)::value;
+        if constexpr (kDma)
+          static_for<g * (A_IT + B_IT) / SEG, (g + 1) * (A_IT + B_IT) / SEG>(
+              [&](auto dc) MOE_INLINE { dma_one(dc, dbuf, ab, bb, live); });
+#pragma unroll
+        for (int c = g * kReads / SEG; c < (g + 1) * kReads / SEG; ++c) read(buf, kk, c, an, bn);
+#pragma unroll
+        for (int m = g * FM * FN / SEG; m < (g + 1) * FM * FN / SEG; ++m)
+          acc[m / FN][m % FN] = mfma_16x16x32(bf[m % FN], af[m / FN], acc[m / FN][m % FN]);
+#pragma unroll
+        for (int c = 0; c < kReads / SEG; ++c) {  // an LDS read, then a share of the products
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x008, FM * FN / kReads, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    };
+    // (two steps to an iteration and the branches of issue() between the halves: with both
+    // halves in one basic block, or one step to an iteration, the register allocator moved
+    // accumulators about on every step)
+    auto main_step = [&](int buf, int s) MOE_INLINE {
+      half(af0, bf0, buf, 1, af1, bf1, std::false_type{}, 0, 0, 0);
       dma_wait_all();
       __syncthreads();
-      if (h + 2 < exts) issue(buf, steps + h + 2);
+      int left = s + 2 - full;
+      asm volatile("" : "+v"(left));
+      const int more = (int)((uint32_t)__builtin_amdgcn_readfirstlane(left) >> 31);
+      if (!more) issue(buf, s + 2);
+      // (past the last step the reads bring what nothing uses)
+      half(af1, bf1, buf ^ 1, 0, af0, bf0, std::true_type{}, buf, more * (s + 2) * 64, more);
+    };
+#pragma unroll 1
+    for (int s = 0; s < steps; s += 2) {
+      main_step(0, s);
+      if (s + 1 < steps) main_step(1, s + 1);
     }
-  }
+
+#pragma unroll 1
+    for (int h = 0; h < exts; ++h) {
+      const int buf = (steps + h) & 1;
+      int left;
+      prepare_ext(h, left);
+      expand(h, buf, left);
+      if (h + 1 < exts) {
+        dma_wait_all();
+        __syncthreads();
+        if (h + 2 < exts) issue(buf, steps + h + 2);
+      }
+    }
   }
   // The tile leaves through LDS (rows of BN bf16, 16-byte chunks XOR-swizzled by the row), so
   // that neighbouring lanes store neighbouring bytes.
@@ -816,15 +816,15 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
 
 int ok() { return hipGetLastError() == hipSuccess ? ST_OK : ST_HIP; }
 
-template <int MT, bool TR, bool LONG>
+template <int MT, bool TR>
 int launch_shrink_ranks(const ShrinkArgs &a, hipStream_t s) {
-  const dim3 grid((a.T + 16 * MT - 1) / (16 * MT) + (TR && a.order ? 1 : 0), LONG ? 1 : 16);
+  const dim3 grid((a.T + 16 * MT - 1) / (16 * MT) + (TR && a.order ? 1 : 0), MT == 1 ? 16 : 1);
   if (a.pool.R <= 16)
-    shrink_kernel<1, MT, TR, LONG><<<grid, kShrinkWaves * 64, 0, s>>>(a);
+    shrink_kernel<1, MT, TR><<<grid, kShrinkWaves * 64, 0, s>>>(a);
   else if (a.pool.R <= 32)
-    shrink_kernel<2, MT, TR, LONG><<<grid, kShrinkWaves * 64, 0, s>>>(a);
+    shrink_kernel<2, MT, TR><<<grid, kShrinkWaves * 64, 0, s>>>(a);
   else
-    shrink_kernel<4, MT, TR, LONG><<<grid, kShrinkWaves * 64, 0, s>>>(a);
+    shrink_kernel<4, MT, TR><<<grid, kShrinkWaves * 64, 0, s>>>(a);
   return ok();
 }
 
@@ -835,7 +835,7 @@ int launch_shrink_ranks(const ShrinkArgs &a, hipStream_t s) {
 // there: four spill (18 us).
 template <bool TR>
 int launch_shrink(const ShrinkArgs &a, hipStream_t s) {
-  return a.T <= 1024 ? launch_shrink_ranks<1, TR, false>(a, s) : launch_shrink_ranks<2, TR, true>(a, s);
+  return a.T <= 1024 ? launch_shrink_ranks<1, TR>(a, s) : launch_shrink_ranks<2, TR>(a, s);
 }
 
 template <int FM, int FN, int W, int G>

@@ -78,7 +78,7 @@ MOE_DEV void pack_block(const RouteArgs &a, int32_t *hist_w, const int32_t *ids_
 
   // ---- stable scatter of this wave's expanded rows.  One workgroup writes final
   // positions; with several, each writes its positions relative to its own block
-  // (into e2p) and the last workgroup to finish adds the global bases.
+  // (into e2p) and the second launch adds the global bases.
   int32_t *start = hist_w + wave * E;
   const int j0 = w_begin * K, j1 = w_end * K;
   const int jl0 = t_begin * K;

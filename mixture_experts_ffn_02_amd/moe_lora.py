@@ -1,6 +1,7 @@
-"""Thin torch-facing binding of the four C calls (argument marshalling only).
+"""Thin torch-facing binding of the C calls (argument marshalling only): the layer's own and the
+operators around it.
 
-PyTorch provides device memory and streams; every step of the layer runs in the HIP
+PyTorch provides device memory and streams; every step runs in the HIP
 kernels of libmoe_lora.so.  Tensors are passed by data pointer: bf16 tensors may be
 ``torch.bfloat16`` or 16-bit integer views of the same bits.
 """
