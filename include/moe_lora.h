@@ -389,7 +389,7 @@ int moe_lora_checkpoint_unpack(int64_t rows, int32_t cols, const uint8_t *codes,
  * or as its checkpoint (y_codes and y_exps of T*k rows, y_perm NULL); giving both or neither
  * is MOE_LORA_ERR_INVALID_ARGUMENT.  The positions are distinct (as moe_lora_route's are).  One
  * outside [0, T*k) takes no part (its weight's gradient is 0); rows that no position names
- * are left as they were. */
+ * are left as they were.  The gradients must not overlap an input. */
 int moe_lora_finalize_backward(const moe_lora_dims *dims, const uint16_t *d_out, const uint16_t *y_perm,
                                const uint8_t *y_codes, const uint8_t *y_exps, const float *topk_weights,
                                const int32_t *expanded_to_permuted, uint16_t *d_y_perm,
@@ -404,7 +404,8 @@ int moe_lora_finalize_backward(const moe_lora_dims *dims, const uint16_t *d_out,
  * at most 2^-16 of it), and y is rounded once.
  *   x [T, in] rows ldx apart, w [out, in], y [T, out] rows ldy apart (columns between are
  *   left as they were), v [T, max_rank] fp32: A x unscaled, zero past a row's rank; written
- *   if not NULL (a backward pass takes it).
+ *   if not NULL (a backward pass takes it; it has to be NULL where num_slots is 0).  y and v
+ *   must not overlap each other or an input.
  * in and out: multiples of 8, in * out < 2^30; ldx and ldy multiples of 8, at most 2^22; T at
  * most 2^24, T * in and T * out at most 2^42 (else MOE_LORA_ERR_UNSUPPORTED).  T may be 0.
  * A token whose slot lies outside [0, num_slots), or whose adapter has rank 0, gets the
@@ -450,7 +451,8 @@ int moe_lora_project(const moe_lora_proj_dims *dims, const uint16_t *x, const ui
  * no adapters).
  *   x: the forward's input in bf16 (rows dims->ldx apart), or its 8-bit checkpoint (x_codes,
  *   x_exps, x NULL); for da only.  w: for dx only.  v: the forward's v; for db only.
- * Giving both forms of x, or neither with da, is MOE_LORA_ERR_INVALID_ARGUMENT.
+ * Giving both forms of x, or neither with da, is MOE_LORA_ERR_INVALID_ARGUMENT.  The gradients
+ * must not overlap each other or an input.
  * Workspace: moe_lora_project_backward_workspace_size bytes, as above. */
 size_t moe_lora_project_backward_workspace_size(const moe_lora_proj_dims *dims, const moe_lora_pool *pool);
 int moe_lora_project_backward(const moe_lora_proj_dims *dims, const uint16_t *x, const uint8_t *x_codes,

@@ -879,7 +879,10 @@ int launch_tiles(const ProjectArgs &a, hipStream_t s) {
 // The largest tiles that still come to most of a round of workgroups; 32 x 32 while all of
 // those run at once, two to a compute unit (dx with adapters, 64 tokens, 4096 -> 2048: 40.4 us
 // in tiles of 64, 28.5 of 32; 512 tokens, 2048 -> 1024, 512 tiles of 32: 21.4 and 19.5; 512,
-// 4096 -> 2048, 1024 tiles: 33.5 and 45).
+// 4096 -> 2048, 1024 tiles: 33.5 and 45).  The 256 x 256 tiles of dx spill registers outside
+// their main loop and are the faster ones all the same (8192 tokens, 2048 -> 4096: 136 us, 161 in
+// tiles of 128; 4096 -> 4096: 250 and 299; 8 mixed adapters: 216 and 239), but for some counts
+// just above a round of workgroups (5000 tokens, 4096 -> 4096, 320 tiles: 222 and 189).
 template <bool NN>
 int launch_product(const ProjectArgs &a, hipStream_t s) {
   auto tiles = [&](int b) { return (long long)((a.T + b - 1) / b) * ((a.N + b - 1) / b); };

@@ -12,7 +12,7 @@
 // rounding to 8 bits is their own; the third term: 4096 tokens of four adapters of rank 32 98.8
 // -> 99.7 us for the call, of eight of rank 64 116 -> 120).  Sums in fp32; an adapter's tokens are added in a fixed
 // order.  Bound by the bytes in flight (4096 tokens, 2048 -> 4096, four adapters of rank 32,
-// x in 8 bits: 18-20 us for 42 MB, against 67 of dx and 18-20 of u).
+// x in 8 bits: 19-21 us for 42 MB, against 66-70 of dx and 19-21 of u).
 #include "checkpoint.h"
 #include "project.h"
 
