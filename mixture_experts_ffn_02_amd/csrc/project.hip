@@ -478,8 +478,8 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
   };
   // A group of the expand holds `per` adapters of up to 32 ranks side by side, or 64 ranks of
   // one: ranks [r0, r0 + 64) of the adapters at [first, first + count) of the list.  (A group
-  // for each adapter: 8192 tokens of 8 mixed adapters of rank 16, 2048 -> 4096: 230 us, 179
-  // so; dx of 64 tokens of 32 adapters 61 us, 40 so.)  It takes two steps over the same rows
+  // for each adapter: 8192 tokens of 8 mixed adapters of rank 16, 2048 -> 4096: 230 us, 170
+  // so; dx of 64 tokens of 32 adapters 61 us, 28 so.)  It takes two steps over the same rows
   // of B: the first terms of s v, then the second.  Where all of the tile's adapters come to
   // 32 ranks (packed) one step does: A holds the first terms in its lower half and the second
   // in its upper, and both meet B's lower half.
@@ -501,10 +501,13 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
     if (packed) term = a_k(0) >> 5;
     const bool live = ext_at(first, count, r0, k, entry, r);
     const uint16_t *src = P.ext_a + (size_t)t0 * 2 * R + term * R + r;
+    int own[A_IT];  // (read before the loads, which nothing is moved across)
+#pragma unroll
+    for (int i = 0; i < A_IT; ++i) own[i] = s_slot[(i * NT + tid) >> 3];
 #pragma unroll
     for (int i = 0; i < A_IT; ++i) {
       const int t = (i * NT + tid) >> 3;
-      const bool on = live && s_slot[t] == list_slot(entry);
+      const bool on = live && own[i] == list_slot(entry);
       const void *z = kZeroChunk, *p = src + (size_t)t * 2 * R;
       dma16(on ? p : z, a_lds(buf) + i * NT * 16);
       if (buf2 >= 0) dma16(on ? static_cast<const uint16_t *>(p) + R : z, a_lds(buf2) + i * NT * 16);
@@ -514,19 +517,22 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
     const char *z = reinterpret_cast<const char *>(kZeroChunk);
     int entry, r;
     const bool live = ext_at(first, count, r0, a_k(0), entry, r);
+    const char *src[B_IT];
 #pragma unroll
     for (int i = 0; i < B_IT; ++i) {
-      const char *src = z;
       if constexpr (!NN) {
         const int n = n0 + ((i * NT + tid) >> 3);
-        if (live && n < N) src = reinterpret_cast<const char *>(P.ext_b + ((size_t)list_slot(entry) * N + n) * R + r);
+        const uint16_t *p = P.ext_b + ((size_t)list_slot(entry) * N + n) * R + r;
+        src[i] = live && n < N ? reinterpret_cast<const char *>(p) : z;
       } else {
         const int q = i * NT + tid, c = (q % BCH) ^ ((((b_k(i) & 3) | ((b_k(i) >> 1) & 4)) & SWZ) << 1);
-        if (ext_at(first, count, r0, b_k(i), entry, r) && n0 + c * 8 < N)
-          src = reinterpret_cast<const char *>(P.ext_b + ((size_t)list_slot(entry) * R + r) * N + n0 + c * 8);
+        const bool on = ext_at(first, count, r0, b_k(i), entry, r) && n0 + c * 8 < N;
+        const uint16_t *p = P.ext_b + ((size_t)list_slot(entry) * R + r) * N + n0 + c * 8;
+        src[i] = on ? reinterpret_cast<const char *>(p) : z;
       }
-      dma16(src, b_lds(buf) + i * NT * 16);
     }
+#pragma unroll
+    for (int i = 0; i < B_IT; ++i) dma16(src[i], b_lds(buf) + i * NT * 16);
   };
 
   f32x4_t acc[FM][FN];
@@ -615,15 +621,18 @@ __global__ __launch_bounds__(WM *WN * 64, BM * BN / (WM * WN) > 8192 ? 1 : 2) vo
       int entry, r;
       ranks = ext_at(first, count, r0, b_k(0), entry, r) ? list_rank(entry) - r : 0;
     }
+    uint32_t ones = 0;  // (an exponent of ones carries into the sign's place)
 #pragma unroll
+    for (int i = 0; i < B_IT; ++i) {
+      const u32x4_t v = *reinterpret_cast<const u32x4_t *>(&Bs[buf][(i * NT + tid) * 8]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) ones |= (v[c] & 0x7f807f80u) + 0x00800080u;
+    }
+    if ((ones & 0x80008000u) == 0u && ranks >= 8) return;
+#pragma unroll 1
     for (int i = 0; i < B_IT; ++i) {
       u32x4_t *p = reinterpret_cast<u32x4_t *>(&Bs[buf][(i * NT + tid) * 8]);
       u32x4_t v = *p;
-      // an exponent of ones carries into the sign's place
-      uint32_t ones = 0;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) ones |= (v[c] & 0x7f807f80u) + 0x00800080u;
-      if ((ones & 0x80008000u) == 0u && ranks >= 8) continue;
       bool change = false;
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
@@ -880,9 +889,9 @@ int launch_tiles(const ProjectArgs &a, hipStream_t s) {
 // those run at once, two to a compute unit (dx with adapters, 64 tokens, 4096 -> 2048: 40.4 us
 // in tiles of 64, 28.5 of 32; 512 tokens, 2048 -> 1024, 512 tiles of 32: 21.4 and 19.5; 512,
 // 4096 -> 2048, 1024 tiles: 33.5 and 45).  The 256 x 256 tiles of dx spill registers outside
-// their main loop and are the faster ones all the same (8192 tokens, 2048 -> 4096: 136 us, 161 in
-// tiles of 128; 4096 -> 4096: 250 and 299; 8 mixed adapters: 216 and 239), but for some counts
-// just above a round of workgroups (5000 tokens, 4096 -> 4096, 320 tiles: 222 and 189).
+// their main loop and are the faster ones all the same (8192 tokens, 2048 -> 4096: 132 us, 161 in
+// tiles of 128; 4096 -> 4096: 245 and 299; 8 mixed adapters: 208 and 239), but for some counts
+// just above a round of workgroups (5000 tokens, 4096 -> 4096, 320 tiles: 212 and 189).
 template <bool NN>
 int launch_product(const ProjectArgs &a, hipStream_t s) {
   auto tiles = [&](int b) { return (long long)((a.T + b - 1) / b) * ((a.N + b - 1) / b); };
