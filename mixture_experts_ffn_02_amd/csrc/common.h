@@ -51,12 +51,13 @@ constexpr size_t kStreamBytes = 128u << 20;
 
 // Workgroups over two grid dimensions: the work-items along one must stay below 2^32 (a launch
 // of more runs what is left of their count, with no error).  block_of_grid: this one's number,
-// which may lie past the last of `blocks`.
+// which may lie past the last of `blocks` (the kernel checks).
+constexpr int kGridRowBits = 20;
 inline dim3 grid_of_blocks(long long blocks) {
-  const long long x = blocks < (1 << 20) ? blocks : (1 << 20);
-  return dim3((unsigned)x, (unsigned)((blocks + x - 1) / x));
+  const long long row = 1ll << kGridRowBits;
+  return dim3((unsigned)(blocks < row ? blocks : row), (unsigned)((blocks + row - 1) / row));
 }
-MOE_DEV long long block_of_grid() { return (long long)blockIdx.y * gridDim.x + blockIdx.x; }
+MOE_DEV long long block_of_grid() { return ((long long)blockIdx.y << kGridRowBits) + blockIdx.x; }
 
 MOE_DEV int lane_id() { return __lane_id(); }
 
